@@ -8,16 +8,25 @@ from .api import (  # noqa: F401
     Config,
     CuRangeStream,
     EpError,
+    balance_loss,
+    balance_loss_backward,
+    balance_workspace_bytes,
     combine,
     combine_ll,
     combine_rank_partial,
     combine_ranks,
     dispatch,
     dispatch_ll,
+    expert_product,
+    expert_product_ll,
+    expert_swiglu,
+    expert_swiglu_ll,
     get_layout,
     get_layout_static,
     get_rank_layout,
     layout_workspace_bytes,
+    mxfp4_dequantize,
+    mxfp4_quantize,
     rank_layout_workspace_bytes,
     route,
     route_layout,

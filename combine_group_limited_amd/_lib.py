@@ -32,6 +32,11 @@ EP_STATIC_SCRATCH_BYTES = 1 << 20
 EP_RECV_FP8_E4M3 = 0
 EP_RECV_BF16 = 1
 
+EP_TYPE_FP8_E4M3 = 0
+EP_TYPE_BF16 = 1
+EP_TYPE_MXFP4 = 2
+EP_TYPE_FP32 = 3
+
 # every function include/ep.h declares
 EXPORTS = (
     "ep_abi_version",
@@ -53,6 +58,15 @@ EXPORTS = (
     "ep_get_rank_layout",
     "ep_combine_rank_partial",
     "ep_combine_ranks",
+    "ep_mxfp4_quantize",
+    "ep_mxfp4_dequantize",
+    "ep_expert_product",
+    "ep_expert_product_ll",
+    "ep_expert_swiglu",
+    "ep_expert_swiglu_ll",
+    "ep_balance_workspace_bytes",
+    "ep_balance_loss",
+    "ep_balance_loss_backward",
     "ep_stream_create_cu_range",
     "ep_stream_destroy",
 )
@@ -130,6 +144,25 @@ def lib() -> ctypes.CDLL:
         L.ep_combine_rank_partial.restype = I
         L.ep_combine_ranks.argtypes = [C, P, P, P, P]
         L.ep_combine_ranks.restype = I
+        I64 = ctypes.c_int64
+        L.ep_mxfp4_quantize.argtypes = [I64, I32, I, P, P, P, P]
+        L.ep_mxfp4_quantize.restype = I
+        L.ep_mxfp4_dequantize.argtypes = [I64, I32, P, P, I, P, P]
+        L.ep_mxfp4_dequantize.restype = I
+        L.ep_expert_product.argtypes = [C, I, I32, I32, P, P, P, P, P, P, P]
+        L.ep_expert_product.restype = I
+        L.ep_expert_product_ll.argtypes = [C, I32, I, I32, I32, P, P, P, P, P, P, P]
+        L.ep_expert_product_ll.restype = I
+        L.ep_expert_swiglu.argtypes = [C, I, I32, I32, P, P, P, P, P, I, P, P, P]
+        L.ep_expert_swiglu.restype = I
+        L.ep_expert_swiglu_ll.argtypes = [C, I32, I, I32, I32, P, P, P, P, P, I, P, P, P]
+        L.ep_expert_swiglu_ll.restype = I
+        L.ep_balance_workspace_bytes.argtypes = [C, I32]
+        L.ep_balance_workspace_bytes.restype = ctypes.c_size_t
+        L.ep_balance_loss.argtypes = [C, P, P, I32, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.ep_balance_loss.restype = I
+        L.ep_balance_loss_backward.argtypes = [C, P, P, P, I32, P, P, P, P, P]
+        L.ep_balance_loss_backward.restype = I
         L.ep_stream_create_cu_range.argtypes = [I, I, ctypes.POINTER(P)]
         L.ep_stream_create_cu_range.restype = I
         L.ep_stream_destroy.argtypes = [P]

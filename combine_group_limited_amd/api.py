@@ -421,6 +421,198 @@ def combine_ranks(cfg: Config, partial: torch.Tensor, rank_slot: torch.Tensor, o
     return out
 
 
+def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """MXFP4 of bf16 or fp32 x [..., cols] (cols a multiple of 32): uint8
+    codes [..., cols/2], two to a byte, and uint8 E8M0 scales [..., cols/32].
+    Expert weights [E, N, K] are quantised in one call."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be a bfloat16 or float32 torch.Tensor")
+    if x.dim() < 1 or x.shape[-1] % 32 or not x.shape[-1]:
+        raise ValueError("x's last dimension must be a positive multiple of 32")
+    dev, cols, lead = x.device, x.shape[-1], tuple(x.shape[:-1])
+    _want(x, "x", x.shape, x.dtype, None)
+    if codes is None:
+        codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=dev)
+    _want(codes, "codes", lead + (cols // 2,), torch.uint8, dev)
+    _want(scales, "scales", lead + (cols // 32,), torch.uint8, dev)
+    kind = L.EP_TYPE_FP32 if x.dtype == torch.float32 else L.EP_TYPE_BF16
+    _check(L.lib().ep_mxfp4_quantize(x.numel() // cols, cols, kind, _ptr(x), _ptr(codes), _ptr(scales),
+                                     _stream(stream, dev)), "ep_mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of MXFP4 codes [..., cols/2] with scales [..., cols/32], as
+    bf16 or fp32 [..., cols]."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dtype must be torch.bfloat16 or torch.float32")
+    if not isinstance(codes, torch.Tensor) or codes.dim() < 1 or codes.shape[-1] % 16 or not codes.shape[-1]:
+        raise ValueError("codes must be a torch.Tensor whose last dimension is a positive multiple of 16")
+    dev, cols, lead = codes.device, codes.shape[-1] * 2, tuple(codes.shape[:-1])
+    _want(codes, "codes", codes.shape, torch.uint8, None)
+    _want(scales, "scales", lead + (cols // 32,), torch.uint8, dev)
+    if out is None:
+        out = torch.empty(lead + (cols,), dtype=dtype, device=dev)
+    _want(out, "out", lead + (cols,), dtype, dev)
+    kind = L.EP_TYPE_FP32 if dtype == torch.float32 else L.EP_TYPE_BF16
+    _check(L.lib().ep_mxfp4_dequantize(codes.numel() // codes.shape[-1], cols, _ptr(codes), _ptr(scales), kind,
+                                       _ptr(out), _stream(stream, dev)), "ep_mxfp4_dequantize")
+    return out
+
+
+def _experts(cfg: Config, capacity, x, x_scales, w, w_scales, rows_of, gate: bool, out_dtype: str, out, out_scales,
+             stream, where: str):
+    """The four experts' products: checks, outputs, and the call.  Rows of x
+    are FP8 with fp32 scales or MXFP4 with uint8 scales, by x_scales' type."""
+    dev = x.device
+    nrows = cfg.nrows if capacity is None else cfg.E * capacity
+    _want(w, "w", (cfg.E,) + tuple(w.shape[1:]), torch.uint8, dev)
+    if w.dim() != 3 or not w.shape[2] or w.shape[2] % 64 or (gate and w.shape[1] % 2):
+        raise ValueError("w must be [E, %s, K/2] bytes, K a multiple of 128" % ("2 * N" if gate else "N"))
+    K, N = 2 * w.shape[2], w.shape[1] // 2 if gate else w.shape[1]
+    _want(w_scales, "w_scales", (cfg.E, w.shape[1], K // 32), torch.uint8, dev)
+    fp8 = x_scales.dtype == torch.float32
+    xb = x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x
+    _want(xb, "x", (nrows, K if fp8 else K // 2), torch.uint8, None)
+    _want(x_scales, "x_scales", (nrows, K // 128 if fp8 else K // 32), torch.float32 if fp8 else torch.uint8, dev)
+    _want(rows_of, "off" if capacity is None else "count", (cfg.E + (capacity is None),), torch.int32, dev)
+    if out_dtype == "bf16":
+        if out is None:
+            out = torch.empty((nrows, N), dtype=torch.bfloat16, device=dev)
+        _want(out, "out", (nrows, N), torch.bfloat16, dev)
+        if out_scales is not None:
+            raise ValueError("out_scales must be None for bf16 output")
+    elif out_dtype == "mxfp4":
+        if out is None:
+            out = torch.empty((nrows, N // 2), dtype=torch.uint8, device=dev)
+        if out_scales is None:
+            out_scales = torch.empty((nrows, N // 32), dtype=torch.uint8, device=dev)
+        _want(out, "out", (nrows, N // 2), torch.uint8, dev)
+        _want(out_scales, "out_scales", (nrows, N // 32), torch.uint8, dev)
+    else:
+        raise ValueError("out_dtype must be 'bf16' or 'mxfp4'")
+    c = cfg.c()
+    args = [ctypes.byref(c)] + ([] if capacity is None else [capacity]) + [
+        L.EP_TYPE_FP8_E4M3 if fp8 else L.EP_TYPE_MXFP4, K, N, _ptr(xb), _ptr(x_scales), _ptr(rows_of), _ptr(w),
+        _ptr(w_scales)]
+    if gate:
+        args += [L.EP_TYPE_MXFP4 if out_dtype == "mxfp4" else L.EP_TYPE_BF16, _ptr(out), _ptr(out_scales)]
+    else:
+        args.append(_ptr(out))
+    _check(getattr(L.lib(), where)(*args, _stream(stream, dev)), where)
+    return (out, out_scales) if out_dtype == "mxfp4" else out
+
+
+def expert_product(cfg: Config, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                   off: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """Each receive row times its expert's weights: bf16 [T*k, N].  x and
+    x_scales as dispatch returns them for FP8 (fp32 scales), or MXFP4 codes
+    [T*k, K/2] with uint8 scales; w, w_scales MXFP4 [E, N, K/2], [E, N, K/32]
+    (mxfp4_quantize of [E, N, K]); off from get_layout.  Rows of no expert are
+    left as they were."""
+    return _experts(cfg, None, x, x_scales, w, w_scales, off, False, "bf16", out, None, stream, "ep_expert_product")
+
+
+def expert_product_ll(cfg: Config, capacity: int, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                      w_scales: torch.Tensor, count: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """expert_product over dispatch_ll's receive rows [E*capacity, ...], with
+    its count."""
+    return _experts(cfg, capacity, x, x_scales, w, w_scales, count, False, "bf16", out, None, stream,
+                    "ep_expert_product_ll")
+
+
+def expert_swiglu(cfg: Config, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                  off: torch.Tensor, out_dtype: str = "bf16", out=None, out_scales=None, stream=None):
+    """The gated product silu(x Wg^T) * (x Wu^T), w [E, 2N, K/2] holding the N
+    gate rows and then the N up rows of each expert: bf16 [T*k, N], or with
+    out_dtype "mxfp4" (codes [T*k, N/2], scales [T*k, N/32]) for the next
+    expert_product."""
+    return _experts(cfg, None, x, x_scales, w, w_scales, off, True, out_dtype, out, out_scales, stream,
+                    "ep_expert_swiglu")
+
+
+def expert_swiglu_ll(cfg: Config, capacity: int, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                     w_scales: torch.Tensor, count: torch.Tensor, out_dtype: str = "bf16", out=None, out_scales=None,
+                     stream=None):
+    """expert_swiglu over dispatch_ll's receive rows, with its count."""
+    return _experts(cfg, capacity, x, x_scales, w, w_scales, count, True, out_dtype, out, out_scales, stream,
+                    "ep_expert_swiglu_ll")
+
+
+def balance_workspace_bytes(cfg: Config, num_seqs: int = 1) -> int:
+    c = cfg.c()
+    return int(L.lib().ep_balance_workspace_bytes(ctypes.byref(c), num_seqs))
+
+
+def _sequences(cfg: Config, logits, seq_offset, token_mask):
+    """Checks shared by the balance loss and its gradient; the number of
+    sequences and the mask as bytes."""
+    _want(logits, "logits", (cfg.T, cfg.E), torch.float32, None)
+    S = 1
+    if seq_offset is not None:
+        if not isinstance(seq_offset, torch.Tensor) or seq_offset.dim() != 1 or seq_offset.numel() < 2:
+            raise ValueError("seq_offset must be a one-dimensional torch.Tensor of at least 2 entries")
+        S = seq_offset.numel() - 1
+        _want(seq_offset, "seq_offset", (S + 1,), torch.int32, logits.device)
+    if token_mask is not None:
+        if isinstance(token_mask, torch.Tensor) and token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        _want(token_mask, "token_mask", (cfg.T,), torch.uint8, logits.device)
+    return S, token_mask
+
+
+def balance_loss(cfg: Config, logits: torch.Tensor, topk_idx: torch.Tensor, seq_offset=None, token_mask=None,
+                 out: dict | None = None, workspace=None, stream=None) -> dict:
+    """Balance loss of the router, by sequence: dict with loss fp32 [S], count
+    int32 [S, E] (picks), ntok int32 [S] (tokens counted) and prob fp32 [S, E]
+    (mean normalised score), and the workspace when the call allocated it.
+    seq_offset int32 [S + 1] bounds the packed sequences (None: one);
+    token_mask [T] (uint8 or bool) is zero for tokens that do not count."""
+    S, mask = _sequences(cfg, logits, seq_offset, token_mask)
+    dev = logits.device
+    _want(topk_idx, "topk_idx", (cfg.T, cfg.k), torch.int32, dev)
+    o = dict(out or {})
+    for name, shape, dtype in (("loss", (S,), torch.float32), ("count", (S, cfg.E), torch.int32),
+                               ("ntok", (S,), torch.int32), ("prob", (S, cfg.E), torch.float32)):
+        if name not in o:
+            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _want(o[name], name, shape, dtype, dev)
+    c = cfg.c()
+    if workspace is None:
+        need = int(L.lib().ep_balance_workspace_bytes(ctypes.byref(c), S))
+        workspace = o["workspace"] = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
+    _check(L.lib().ep_balance_loss(ctypes.byref(c), _ptr(logits), _ptr(topk_idx), S, _ptr(seq_offset), _ptr(mask),
+                                   _ptr(o["loss"]), _ptr(o["count"]), _ptr(o["ntok"]), _ptr(o["prob"]),
+                                   _ptr(workspace), workspace.numel(), _stream(stream, dev)), "ep_balance_loss")
+    return o
+
+
+def balance_loss_backward(cfg: Config, logits: torch.Tensor, count: torch.Tensor, ntok: torch.Tensor,
+                          grad_loss: torch.Tensor, seq_offset=None, token_mask=None, grad_logits=None,
+                          stream=None) -> torch.Tensor:
+    """Gradient of sum(grad_loss * loss) with respect to the logits, fp32
+    [T, E], with the counts as constants; count and ntok from balance_loss,
+    grad_loss fp32 [S].  `grad_logits` may be `logits` itself (in place)."""
+    S, mask = _sequences(cfg, logits, seq_offset, token_mask)
+    dev = logits.device
+    _want(count, "count", (S, cfg.E), torch.int32, dev)
+    _want(ntok, "ntok", (S,), torch.int32, dev)
+    _want(grad_loss, "grad_loss", (S,), torch.float32, dev)
+    if grad_logits is None:
+        grad_logits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=dev)
+    _want(grad_logits, "grad_logits", (cfg.T, cfg.E), torch.float32, dev)
+    c = cfg.c()
+    _check(L.lib().ep_balance_loss_backward(ctypes.byref(c), _ptr(logits), _ptr(count), _ptr(ntok), S,
+                                            _ptr(seq_offset), _ptr(mask), _ptr(grad_loss), _ptr(grad_logits),
+                                            _stream(stream, dev)), "ep_balance_loss_backward")
+    return grad_logits
+
+
 class CuRangeStream:
     """A HIP stream confined to compute units [first_cu, first_cu + num_cus)
     (ep_stream_create_cu_range), usable as `stream=` here and, through

@@ -28,7 +28,8 @@ CHECK_SOURCES = ["selfcheck.hip"]
 # next to it by build(); the loader compares it with the current sources
 HASH_PATH = LIB_PATH + ".sources"
 
-SOURCES = ["api.hip", "gate.hip", "layout.hip", "dispatch.hip", "combine.hip", "ll.hip"]
+SOURCES = ["api.hip", "gate.hip", "layout.hip", "dispatch.hip", "combine.hip", "ll.hip", "quant.hip",
+           "experts.hip", "balance.hip"]
 HEADERS = ["device.h", "launch.h", "rows.h"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

@@ -83,6 +83,31 @@ int validate_ll(const ep_config_t* c, int32_t capacity) {
     return EP_OK;
 }
 
+constexpr int32_t kMaxSeqs = 65536;
+constexpr int32_t kMaxFeatures = 32768;
+constexpr int32_t kMaxBlockCols = 1 << 20;
+
+// rows, columns and pointers of the MXFP4 conversions
+int validate_mx(int64_t rows, int32_t cols, int type, const void* wide, const void* codes, const void* scales) {
+    if (rows < 0 || cols < 32 || cols % 32 != 0) return EP_ERR_INVALID_ARG;
+    if (type != EP_TYPE_BF16 && type != EP_TYPE_FP32) return EP_ERR_INVALID_ARG;
+    if (cols > kMaxBlockCols || rows > (1L << 40)) return EP_ERR_UNSUPPORTED;
+    if (rows > 0 && (!wide || !codes || !scales)) return EP_ERR_INVALID_ARG;
+    if (!aligned(wide, 16) || !aligned(codes, 16)) return EP_ERR_ALIGNMENT;
+    return EP_OK;
+}
+
+// sequences, mask and logits of the balance loss
+int validate_balance(const ep_config_t* cfg, int32_t num_seqs, const int32_t* seq_offset, const float* logits) {
+    const int rc = validate(cfg);
+    if (rc) return rc;
+    if (num_seqs < 1 || (!seq_offset && num_seqs != 1)) return EP_ERR_INVALID_ARG;
+    if (num_seqs > kMaxSeqs) return EP_ERR_UNSUPPORTED;
+    if (cfg->num_tokens > 0 && !logits) return EP_ERR_INVALID_ARG;
+    if (!aligned(logits, 4) || !aligned(seq_offset, 4)) return EP_ERR_ALIGNMENT;
+    return EP_OK;
+}
+
 ep::Shape shape_of(const ep_config_t* c) {
     return ep::Shape{c->num_tokens, c->hidden,    c->num_experts, c->num_groups,
                      c->topk_groups, c->topk, c->num_ranks,   effective_topm(c)};
@@ -92,6 +117,26 @@ int hip_status(hipError_t e) {
     if (e == hipSuccess) return EP_OK;
     g_last_hip_error = (int)e;
     return EP_ERR_HIP;
+}
+
+// an experts' product over packed (capacity 0) or fixed-capacity rows, the
+// configuration validated
+int expert_product(const ep_config_t* cfg, int32_t capacity, int x_type, int32_t K, int32_t N, const void* x,
+                   const void* x_scales, const int32_t* list, const void* w, const uint8_t* w_scales, bool gate,
+                   int y_type, void* y, uint8_t* y_scales, void* stream) {
+    if (x_type != EP_TYPE_FP8_E4M3 && x_type != EP_TYPE_MXFP4) return EP_ERR_INVALID_ARG;
+    if (y_type != EP_TYPE_BF16 && y_type != EP_TYPE_MXFP4) return EP_ERR_INVALID_ARG;
+    if (K < 128 || K % 128 != 0 || N < 32 || N % 32 != 0) return EP_ERR_INVALID_ARG;
+    const bool mx_out = y_type == EP_TYPE_MXFP4;
+    if (!mx_out && y_scales) return EP_ERR_INVALID_ARG;
+    if (K > kMaxFeatures || N > (gate ? kMaxFeatures / 2 : kMaxFeatures)) return EP_ERR_UNSUPPORTED;
+    if (!list || !w || !w_scales) return EP_ERR_INVALID_ARG;
+    if (cfg->num_tokens > 0 && (!x || !x_scales || !y || (mx_out && !y_scales))) return EP_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(x_scales, 4) || !aligned(list, 4) || !aligned(w, 16) || !aligned(y, 16))
+        return EP_ERR_ALIGNMENT;
+    return hip_status(ep::launch_expert_product(
+        shape_of(cfg), capacity, x_type == EP_TYPE_FP8_E4M3, gate, mx_out, K, N, static_cast<const uint8_t*>(x),
+        x_scales, list, static_cast<const uint8_t*>(w), w_scales, y, y_scales, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -348,6 +393,94 @@ EP_API int ep_combine_ranks(const ep_config_t* cfg, const void* partial, const i
     if (!aligned(partial, 16) || !aligned(out, 16) || !aligned(rank_slot, 4)) return EP_ERR_ALIGNMENT;
     return hip_status(ep::launch_combine_ranks(shape_of(cfg), static_cast<const uint16_t*>(partial), rank_slot,
                                                static_cast<uint16_t*>(out), static_cast<hipStream_t>(stream)));
+}
+
+EP_API int ep_mxfp4_quantize(int64_t rows, int32_t cols, int x_type, const void* x, void* codes, uint8_t* scales,
+                             void* stream) {
+    const int rc = validate_mx(rows, cols, x_type, x, codes, scales);
+    if (rc) return rc;
+    return hip_status(ep::launch_mxfp4_quantize(rows * (cols / 32), x_type == EP_TYPE_FP32, x,
+                                                static_cast<uint8_t*>(codes), scales,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+EP_API int ep_mxfp4_dequantize(int64_t rows, int32_t cols, const void* codes, const uint8_t* scales, int out_type,
+                               void* out, void* stream) {
+    const int rc = validate_mx(rows, cols, out_type, out, codes, scales);
+    if (rc) return rc;
+    return hip_status(ep::launch_mxfp4_dequantize(rows * (cols / 32), out_type == EP_TYPE_FP32,
+                                                  static_cast<const uint8_t*>(codes), scales, out,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+EP_API int ep_expert_product(const ep_config_t* cfg, int x_type, int32_t in_features, int32_t out_features,
+                             const void* x, const void* x_scales, const int32_t* expert_offset, const void* w,
+                             const uint8_t* w_scales, void* y, void* stream) {
+    const int rc = validate(cfg);
+    if (rc) return rc;
+    return expert_product(cfg, 0, x_type, in_features, out_features, x, x_scales, expert_offset, w, w_scales, false,
+                          EP_TYPE_BF16, y, nullptr, stream);
+}
+
+EP_API int ep_expert_product_ll(const ep_config_t* cfg, int32_t capacity, int x_type, int32_t in_features,
+                                int32_t out_features, const void* x, const void* x_scales, const int32_t* recv_count,
+                                const void* w, const uint8_t* w_scales, void* y, void* stream) {
+    const int rc = validate_ll(cfg, capacity);
+    if (rc) return rc;
+    return expert_product(cfg, capacity, x_type, in_features, out_features, x, x_scales, recv_count, w, w_scales,
+                          false, EP_TYPE_BF16, y, nullptr, stream);
+}
+
+EP_API int ep_expert_swiglu(const ep_config_t* cfg, int x_type, int32_t in_features, int32_t out_features,
+                            const void* x, const void* x_scales, const int32_t* expert_offset, const void* w,
+                            const uint8_t* w_scales, int y_type, void* y, uint8_t* y_scales, void* stream) {
+    const int rc = validate(cfg);
+    if (rc) return rc;
+    return expert_product(cfg, 0, x_type, in_features, out_features, x, x_scales, expert_offset, w, w_scales, true,
+                          y_type, y, y_scales, stream);
+}
+
+EP_API int ep_expert_swiglu_ll(const ep_config_t* cfg, int32_t capacity, int x_type, int32_t in_features,
+                               int32_t out_features, const void* x, const void* x_scales, const int32_t* recv_count,
+                               const void* w, const uint8_t* w_scales, int y_type, void* y, uint8_t* y_scales,
+                               void* stream) {
+    const int rc = validate_ll(cfg, capacity);
+    if (rc) return rc;
+    return expert_product(cfg, capacity, x_type, in_features, out_features, x, x_scales, recv_count, w, w_scales,
+                          true, y_type, y, y_scales, stream);
+}
+
+EP_API size_t ep_balance_workspace_bytes(const ep_config_t* cfg, int32_t num_seqs) {
+    if (validate(cfg) || num_seqs < 1 || num_seqs > kMaxSeqs) return 0;
+    return ep::balance_workspace_bytes(shape_of(cfg), num_seqs);
+}
+
+EP_API int ep_balance_loss(const ep_config_t* cfg, const float* logits, const int32_t* topk_idx, int32_t num_seqs,
+                           const int32_t* seq_offset, const uint8_t* token_mask, float* loss, int32_t* count,
+                           int32_t* ntok, float* prob, void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = validate_balance(cfg, num_seqs, seq_offset, logits);
+    if (rc) return rc;
+    if (!loss || !count || !ntok || !prob || (cfg->num_tokens > 0 && !topk_idx)) return EP_ERR_INVALID_ARG;
+    if (!aligned(topk_idx, 4) || !aligned(loss, 4) || !aligned(count, 4) || !aligned(ntok, 4) || !aligned(prob, 4))
+        return EP_ERR_ALIGNMENT;
+    const ep::Shape s = shape_of(cfg);
+    if (!workspace || workspace_bytes < ep::balance_workspace_bytes(s, num_seqs)) return EP_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return EP_ERR_ALIGNMENT;
+    return hip_status(ep::launch_balance_loss(s, logits, topk_idx, num_seqs, seq_offset, token_mask, loss, count,
+                                              ntok, prob, workspace, static_cast<hipStream_t>(stream)));
+}
+
+EP_API int ep_balance_loss_backward(const ep_config_t* cfg, const float* logits, const int32_t* count,
+                                    const int32_t* ntok, int32_t num_seqs, const int32_t* seq_offset,
+                                    const uint8_t* token_mask, const float* grad_loss, float* grad_logits,
+                                    void* stream) {
+    const int rc = validate_balance(cfg, num_seqs, seq_offset, logits);
+    if (rc) return rc;
+    if (!count || !ntok || !grad_loss || (cfg->num_tokens > 0 && !grad_logits)) return EP_ERR_INVALID_ARG;
+    if (!aligned(count, 4) || !aligned(ntok, 4) || !aligned(grad_loss, 4) || !aligned(grad_logits, 4))
+        return EP_ERR_ALIGNMENT;
+    return hip_status(ep::launch_balance_grad(shape_of(cfg), logits, num_seqs, seq_offset, token_mask, count, ntok,
+                                              grad_loss, grad_logits, static_cast<hipStream_t>(stream)));
 }
 
 EP_API int ep_stream_create_cu_range(int first_cu, int num_cus, void** stream) {

@@ -1,0 +1,458 @@
+// balance.hip -- the router's balance loss, its per-expert counts, and its
+// gradient with respect to the logits.
+//
+// For a sequence of n counted tokens, with s the gate's sigmoid scores:
+//   p[t,e]  = s[t,e] / sum_j s[t,j]         (0 where the sum is 0)
+//   P[e]    = (1/n) sum_t p[t,e]
+//   f[e]    = E / (k n) * count[e]          count[e] = picks of e
+//   loss    = sum_e f[e] P[e]
+// The counts are constants of the gradient.  With c[e] = f[e] / n,
+// dp/ds = (delta - p) / sum s and ds/dlogit = s (1 - s):
+//   dlogit[t,e] = g (c[e] - sum_j c[j] p[t,j]) p[t,e] (1 - s[t,e])
+// 1 - s is taken as exp(-x) s, which keeps its digits where s is close to 1.
+//
+// Both directions walk the tokens in chunks of consecutive tokens, one chunk
+// to a workgroup.  A chunk may hold ends of sequences; its tokens of one
+// sequence are a segment.  (chunk + sequence) differs between segments
+// (along the tokens one of the two grows at every step), so it numbers the
+// segments' partial sums, chunks + sequences of them at most.  A second
+// launch sums each sequence's segments in order: no floating-point atomics,
+// the same bits on every run.
+//
+// A token belongs to LPT lanes (16, 32 or 64), which hold its logits in
+// registers, so a logit is read once by each direction.
+#include "device.h"
+#include "launch.h"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 256;   // of the token kernels
+constexpr int kMinChunk = 16;   // tokens per workgroup at least
+constexpr int kChunks = 512;    // workgroups aimed at for long batches
+constexpr int kRunning = 32;    // tokens summed before they join the longer sum
+constexpr int kSlice = 64;      // experts per workgroup of the summing launch
+constexpr int kParts = 16;      // segments it sums side by side
+
+// 1 - sigmoid(x) for any x: 1 - s below 0, and e / (1 + e) with e = exp(-x)
+// above, where e is carried into the subnormal numbers (cw_expf cuts it there)
+// by one ldexp; it is 0 from x = 104 on.
+__device__ __forceinline__ float sigmoid_rest(float x, float s) {
+    const float z = x > 0.0f ? __builtin_fmaxf(-x, -110.0f) : 0.0f;
+    const float n = __builtin_rintf(z * 0x1.715476p+0f);
+    float r = __builtin_fmaf(-n, 0x1.62ep-1f, z);
+    r = __builtin_fmaf(-n, 0x1.0bfbe8p-15f, r);
+    float p = 0x1.a01a02p-13f;  // 1/7!, 1/6!, ... as in cw_expf
+    p = __builtin_fmaf(p, r, 0x1.6c16c2p-10f);
+    p = __builtin_fmaf(p, r, 0x1.111112p-7f);
+    p = __builtin_fmaf(p, r, 0x1.555556p-5f);
+    p = __builtin_fmaf(p, r, 0x1.555556p-3f);
+    p = __builtin_fmaf(p, r, 0.5f);
+    p = __builtin_fmaf(p, r, 1.0f);
+    p = __builtin_fmaf(p, r, 1.0f);
+    const float e = __builtin_ldexpf(p, (int)n);
+    return x > 0.0f ? e / (1.0f + e) : 1.0f - s;
+}
+
+// sigmoid(x) and 1 - sigmoid(x) of N values of a lane; scores as the gate has
+// them (the short form within kSigmoidFastBound, see device.h).
+template <int N>
+__device__ __forceinline__ void sigmoid_both(float (&s)[N], float (&r)[N]) {
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ok = ok && __builtin_fabsf(s[i]) <= kSigmoidFastBound;
+    if (__all(ok)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float e;
+            s[i] = sigmoid_inrange(s[i], e);
+            r[i] = e * s[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float x = s[i];
+            s[i] = sigmoid(x);
+            r[i] = sigmoid_rest(x, s[i]);
+        }
+    }
+}
+
+// Sum over the LPT lanes of a token (xor butterfly: every lane gets it, in
+// the same order).
+template <int LPT>
+__device__ __forceinline__ float token_sum(float v) {
+    v += __uint_as_float(partner_u32<1>(__float_as_uint(v)));
+    v += __uint_as_float(partner_u32<2>(__float_as_uint(v)));
+    v += __uint_as_float(partner_u32<4>(__float_as_uint(v)));
+    v += __uint_as_float(partner_u32<8>(__float_as_uint(v)));
+    if constexpr (LPT > 16) v += __uint_as_float(partner_u32<16>(__float_as_uint(v)));
+    if constexpr (LPT > 32) v += __uint_as_float(partner_u32<32>(__float_as_uint(v)));
+    return v;
+}
+
+// How a token's E values lie over its lanes: N runs of LPT lanes x W values.
+template <int LPT_, int N_, int W_>
+struct Lanes {
+    static constexpr int LPT = LPT_, N = N_, W = W_, V = N_ * W_;
+    static constexpr int kTokens = kThreads / LPT_;  // tokens side by side
+
+    __device__ static __forceinline__ int expert(int i, int sub) { return ((i / W) * LPT + sub) * W + i % W; }
+
+    // values of a row of E, zero beyond it
+    __device__ static __forceinline__ void load(const float* row, int E, int sub, float (&v)[V]) {
+        const auto r = buffer_rsrc(row, (uint32_t)E * 4u);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (W == 4) {
+                const i32x4 q = __builtin_amdgcn_raw_buffer_load_b128(r, (i * LPT + sub) * 16, 0, kCached);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i * 4 + j] = __int_as_float(q[j]);
+            } else {
+                v[i] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (i * LPT + sub) * 4, 0, kCached));
+            }
+        }
+    }
+
+    // zero beyond the row (the scores of the zeros that load leaves there)
+    __device__ static __forceinline__ void cut(int E, int sub, float (&v)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = expert(i, sub) < E ? v[i] : 0.0f;
+    }
+
+    __device__ static __forceinline__ void store(float* row, int E, int sub, const float (&v)[V]) {
+        const auto r = buffer_rsrc(row, (uint32_t)E * 4u);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (W == 4) {
+                i32x4 q;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[j] = __float_as_int(v[i * 4 + j]);
+                __builtin_amdgcn_raw_buffer_store_b128(q, r, (i * LPT + sub) * 16, 0, kStream);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v[i]), r, (i * LPT + sub) * 4, 0, kStream);
+            }
+        }
+    }
+};
+
+// Sequence boundaries as the kernels use them: clamped to [0, T], so that no
+// list of offsets leads outside the batch.  A null list is one sequence of
+// all tokens.
+struct Sequences {
+    const int32_t* off;
+    int S, T;
+    __device__ __forceinline__ int at(int s) const {
+        if (!off) return s > 0 ? T : 0;
+        const int v = off[s];
+        return v < 0 ? 0 : (v > T ? T : v);
+    }
+    // the last sequence that starts at or before token t (-1: none), found
+    // 64 ways at a time by a whole wavefront
+    __device__ __forceinline__ int find(int t) const {
+        int lo = -1, n = S;  // starts lo + 1 .. lo + n are undecided
+        while (n > 0) {
+            const int step = (n + 63) >> 6;
+            const int i = lo + ((int)(threadIdx.x & 63) + 1) * step;  // last of this lane's run
+            const bool before = i < S && i <= lo + n && at(i) <= t;
+            const int runs = __popcll(__ballot(before));
+            const int last = lo + n;
+            lo += runs * step;
+            n = min(step - 1, last - lo);
+        }
+        return lo;
+    }
+};
+
+__device__ __forceinline__ bool counted(const uint8_t* __restrict__ mask, int t) { return !mask || mask[t] != 0; }
+
+// Partial sums of a segment: probabilities and picks by expert, and tokens.
+struct Partials {
+    float* prob;     // [slots, E]
+    int32_t* count;  // [slots, E]
+    int32_t* tokens; // [slots]
+    float* loss;     // [S, slices]
+    uint32_t* done;  // [S] slices finished
+};
+
+template <class L>
+__global__ __launch_bounds__(kThreads) void balance_partial_kernel(const float* __restrict__ logits,
+                                                                   const int32_t* __restrict__ idx,
+                                                                   const uint8_t* __restrict__ mask, Sequences seq,
+                                                                   Partials out, int T, int E, int k, int chunk) {
+    constexpr int LPT = L::LPT, V = L::V;
+    __shared__ float sum[L::kTokens * LPT * V];
+    __shared__ int32_t hist[LPT * V];
+    __shared__ int32_t tokens;
+    const int tid = threadIdx.x, sub = tid % LPT, slot = tid / LPT;
+    const int t0 = blockIdx.x * chunk, t1 = min(T, t0 + chunk);
+    for (int i = blockIdx.x * kThreads + tid; i < seq.S; i += gridDim.x * kThreads) out.done[i] = 0u;
+
+    for (int s = max(seq.find(t0), 0); s < seq.S; ++s) {
+        const int first = seq.at(s);
+        if (first >= t1) break;
+        const int b = max(t0, first), e = min(t1, seq.at(s + 1));
+        if (e <= b) continue;
+        for (int i = tid; i < E; i += kThreads) hist[i] = 0;
+        if (tid == 0) tokens = 0;
+        __syncthreads();
+
+        float acc[V], run[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = run[i] = 0.0f;
+        int n = 0, held = 0;
+        for (int t = b + slot; t < e; t += L::kTokens) {
+            const bool on = counted(mask, t);
+            float v[V];
+            L::load(logits + (size_t)t * E, E, sub, v);
+            sigmoid_lane(v);
+            L::cut(E, sub, v);
+            float z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) z += v[i];
+            z = token_sum<LPT>(z);
+            const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+            for (int i = 0; i < V; ++i) run[i] += on ? v[i] * inv : 0.0f;
+            n += on ? 1 : 0;
+            if (++held == kRunning) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += run[i], run[i] = 0.0f;
+                held = 0;
+            }
+        }
+        if (sub == 0 && n) atomicAdd(&tokens, n);
+        for (int i = tid; i < (e - b) * k; i += kThreads) {
+            const int t = b + i / k;
+            const int x = idx[(size_t)b * k + i];
+            if ((unsigned)x < (unsigned)E && counted(mask, t)) atomicAdd(&hist[x], 1);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[slot * (LPT * V) + L::expert(i, sub)] = acc[i] + run[i];
+        __syncthreads();
+        const size_t row = (size_t)blockIdx.x + s;
+        for (int i = tid; i < E; i += kThreads) {
+            float p = 0.0f;
+#pragma unroll
+            for (int j = 0; j < L::kTokens; ++j) p += sum[j * (LPT * V) + i];
+            out.prob[row * E + i] = p;
+            out.count[row * E + i] = hist[i];
+        }
+        if (tid == 0) out.tokens[row] = tokens;
+        __syncthreads();
+    }
+}
+
+// One workgroup sums kSlice experts of one sequence: kParts groups of threads
+// take the segments in turn, then their sums are added in order.  The last
+// workgroup of a sequence adds the slices' shares of its loss, in order.
+__global__ __launch_bounds__(kSlice * kParts) void balance_sum_kernel(Partials in, Sequences seq, int E, int k,
+                                                                      int chunk, float* __restrict__ loss,
+                                                                      int32_t* __restrict__ count,
+                                                                      int32_t* __restrict__ ntok,
+                                                                      float* __restrict__ prob) {
+    __shared__ double psum[kParts][kSlice];
+    __shared__ int32_t csum[kParts][kSlice];
+    __shared__ int32_t nsum[kParts];
+    const int tid = threadIdx.x, col = tid % kSlice, part = tid / kSlice;
+    const int slices = (E + kSlice - 1) / kSlice, slice = blockIdx.x % slices;
+    const int s = blockIdx.x / slices, e = slice * kSlice + col;
+    const int b = seq.at(s), end = seq.at(s + 1);
+    double p = 0.0;
+    int32_t c = 0, n = 0;
+    if (end > b) {
+        const int last = (end - 1) / chunk;
+        for (int g = b / chunk + part; g <= last; g += kParts) {
+            const size_t row = (size_t)g + s;
+            if (e < E) {
+                p += (double)in.prob[row * E + e];
+                c += in.count[row * E + e];
+            }
+            n += in.tokens[row];
+        }
+    }
+    psum[part][col] = p;
+    csum[part][col] = c;
+    if (col == 0) nsum[part] = n;
+    __syncthreads();
+    if (part != 0) return;
+    p = 0.0, c = 0, n = 0;
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) p += psum[j][col], c += csum[j][col], n += nsum[j];
+    double share = 0.0;
+    if (e < E) {
+        p = n ? p / n : 0.0;
+        share = n ? p * c * E / ((double)k * n) : 0.0;
+        prob[(size_t)s * E + e] = (float)p;
+        count[(size_t)s * E + e] = c;
+    }
+    if (slice == 0 && tid == 0) ntok[s] = n;
+    // the first wavefront is all that is left: its 64 shares, by butterfly
+#pragma unroll
+    for (int d = 1; d < kSlice; d <<= 1) share += __shfl_xor(share, d, kWave);
+    if (tid == 0) {
+        if (slices == 1) {
+            loss[s] = (float)share;
+            return;
+        }
+        float* mine = in.loss + (size_t)s * slices;
+        __hip_atomic_store(&mine[slice], (float)share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (__hip_atomic_fetch_add(&in.done[s], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+            (uint32_t)slices - 1u) {
+            double l = 0.0;
+            for (int i = 0; i < slices; ++i)
+                l += (double)__hip_atomic_load(&mine[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            loss[s] = (float)l;
+        }
+    }
+}
+
+template <class L>
+__global__ __launch_bounds__(kThreads) void balance_grad_kernel(const float* logits,
+                                                                const uint8_t* __restrict__ mask, Sequences seq,
+                                                                const int32_t* __restrict__ count,
+                                                                const int32_t* __restrict__ ntok,
+                                                                const float* __restrict__ grad_loss,
+                                                                float* grad, int T, int E, int k, int chunk) {
+    constexpr int LPT = L::LPT, V = L::V;
+    const int sub = threadIdx.x % LPT, slot = threadIdx.x / LPT;
+    const int t0 = blockIdx.x * chunk, t1 = min(T, t0 + chunk);
+    float zero[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) zero[i] = 0.0f;
+
+    int at = t0;  // tokens before it have their gradient
+    for (int s = max(seq.find(t0), 0); s < seq.S && at < t1; ++s) {
+        const int first = seq.at(s);
+        if (first >= t1) break;
+        const int b = max(at, first), e = min(t1, seq.at(s + 1));
+        if (e <= b) continue;
+        for (int t = at + slot; t < b; t += L::kTokens) L::store(grad + (size_t)t * E, E, sub, zero);  // in no sequence
+        // g c[e], with c[e] = E count / (k n^2)
+        const int n = ntok[s];
+        const double per = n > 0 ? (double)grad_loss[s] * E / ((double)k * n * n) : 0.0;
+        float c[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int x = L::expert(i, sub);
+            c[i] = x < E ? (float)(per * count[(size_t)s * E + x]) : 0.0f;
+        }
+        for (int t = b + slot; t < e; t += L::kTokens) {
+            const bool on = counted(mask, t);
+            float v[V], r[V];
+            L::load(logits + (size_t)t * E, E, sub, v);
+            sigmoid_both(v, r);
+            L::cut(E, sub, v);
+            float z = 0.0f, m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) z += v[i];
+            z = token_sum<LPT>(z);
+            const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[i] *= inv;
+                m = __builtin_fmaf(c[i], v[i], m);
+            }
+            m = token_sum<LPT>(m);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = on ? (c[i] - m) * (v[i] * r[i]) : 0.0f;
+            L::store(grad + (size_t)t * E, E, sub, v);
+        }
+        at = e;
+    }
+    for (int t = at + slot; t < t1; t += L::kTokens) L::store(grad + (size_t)t * E, E, sub, zero);
+}
+
+// Tokens per workgroup: 16 up to 8192 tokens (256 workgroups at 4096), then
+// as many as leave kChunks workgroups.
+int chunk_of(int T) {
+    const int c = (T + kChunks - 1) / kChunks;
+    return c <= kMinChunk ? kMinChunk : (c + kMinChunk - 1) / kMinChunk * kMinChunk;
+}
+
+int chunks_of(int T) { return (T + chunk_of(T) - 1) / chunk_of(T); }
+int slices_of(int E) { return (E + kSlice - 1) / kSlice; }
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+Partials partials(const Shape& s, int S, void* ws, size_t* bytes) {
+    const size_t slots = (size_t)chunks_of(s.T) + S;
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    size_t at = 0;
+    const auto take = [&](size_t n) {
+        uint8_t* q = p + at;
+        at += up256(n);
+        return q;
+    };
+    Partials r;
+    r.prob = reinterpret_cast<float*>(take(slots * s.E * 4));
+    r.count = reinterpret_cast<int32_t*>(take(slots * s.E * 4));
+    r.tokens = reinterpret_cast<int32_t*>(take(slots * 4));
+    r.loss = reinterpret_cast<float*>(take((size_t)S * slices_of(s.E) * 4));
+    r.done = reinterpret_cast<uint32_t*>(take((size_t)S * 4));
+    if (bytes) *bytes = at;
+    return r;
+}
+
+// Runs `f` with the lanes that fit E: 16-byte pieces of a row need E a
+// multiple of 4 and 16-byte aligned rows.
+template <class F>
+hipError_t with_lanes(int E, bool vec, F f) {
+    if (vec) {
+        if (E <= 64) return f(Lanes<16, 1, 4>());
+        if (E <= 128) return f(Lanes<32, 1, 4>());
+        if (E <= 256) return f(Lanes<64, 1, 4>());
+        if (E <= 512) return f(Lanes<64, 2, 4>());
+        return f(Lanes<64, 4, 4>());
+    }
+    if (E <= 16) return f(Lanes<16, 1, 1>());
+    if (E <= 64) return f(Lanes<64, 1, 1>());
+    if (E <= 256) return f(Lanes<64, 4, 1>());
+    return f(Lanes<64, 16, 1>());
+}
+
+bool aligned16(const void* a, const void* b) {
+    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+}
+
+}  // namespace
+
+size_t balance_workspace_bytes(const Shape& s, int S) {
+    size_t n = 0;
+    partials(s, S, nullptr, &n);
+    return n;
+}
+
+hipError_t launch_balance_loss(const Shape& s, const float* logits, const int32_t* idx, int S, const int32_t* off,
+                               const uint8_t* mask, float* loss, int32_t* count, int32_t* ntok, float* prob, void* ws,
+                               hipStream_t stream) {
+    const Partials p = partials(s, S, ws, nullptr);
+    const Sequences seq{off, S, s.T};
+    const int chunk = chunk_of(s.T);
+    // an empty batch still gets its one workgroup, which clears `done`
+    const int grid = s.T > 0 ? chunks_of(s.T) : 1;
+    const hipError_t e = with_lanes(s.E, s.E % 4 == 0 && aligned16(logits, logits), [&](auto lanes) {
+        hipLaunchKernelGGL(balance_partial_kernel<decltype(lanes)>, dim3(grid), dim3(kThreads), 0, stream, logits, idx,
+                           mask, seq, p, s.T, s.E, s.k, chunk);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(balance_sum_kernel, dim3(slices_of(s.E) * S), dim3(kSlice * kParts), 0, stream, p, seq, s.E, s.k,
+                       chunk, loss, count, ntok, prob);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_grad(const Shape& s, const float* logits, int S, const int32_t* off, const uint8_t* mask,
+                               const int32_t* count, const int32_t* ntok, const float* grad_loss, float* grad,
+                               hipStream_t stream) {
+    if (s.T == 0) return hipSuccess;
+    const Sequences seq{off, S, s.T};
+    return with_lanes(s.E, s.E % 4 == 0 && aligned16(logits, grad), [&](auto lanes) {
+        hipLaunchKernelGGL(balance_grad_kernel<decltype(lanes)>, dim3(chunks_of(s.T)), dim3(kThreads), 0, stream,
+                           logits, mask, seq, count, ntok, grad_loss, grad, s.T, s.E, s.k, chunk_of(s.T));
+        return hipGetLastError();
+    });
+}
+
+}  // namespace ep

@@ -99,7 +99,8 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + cw_exp
 // all 2,235,564,034 fp32 values with |x| <= 80.
 constexpr float kSigmoidFastBound = 80.0f;
 
-__device__ __forceinline__ float sigmoid_inrange(float x) {
+// The two-argument form also gives exp(-x).
+__device__ __forceinline__ float sigmoid_inrange(float x, float& ex) {
     const float L2E = 0x1.715476p+0f;
     const float C1 = 0x1.62ep-1f;
     const float C2 = 0x1.0bfbe8p-15f;
@@ -115,9 +116,15 @@ __device__ __forceinline__ float sigmoid_inrange(float x) {
     p = __builtin_fmaf(p, r, 0.5f);
     p = __builtin_fmaf(p, r, 1.0f);
     p = __builtin_fmaf(p, r, 1.0f);
-    const float y = 1.0f + __builtin_ldexpf(p, (int)n);
+    ex = __builtin_ldexpf(p, (int)n);
+    const float y = 1.0f + ex;
     const float q = __builtin_amdgcn_rcpf(y);
     return __builtin_fmaf(__builtin_fmaf(-y, q, 1.0f), q, q);
+}
+
+__device__ __forceinline__ float sigmoid_inrange(float x) {
+    float ex;
+    return sigmoid_inrange(x, ex);
 }
 
 // In place: sigmoid of the N values one lane holds.  The short form runs

@@ -71,6 +71,29 @@ hipError_t launch_dispatch_ll(const Shape& s, int cap, bool fp8, const uint16_t*
                               void* recv, float* recv_scales, int32_t* recv_count, int32_t* recv_src,
                               int32_t* slot, hipStream_t stream);
 
+// MXFP4 (quant.hip): `blocks` runs of 32 values; wide = 32-bit values, else bf16
+hipError_t launch_mxfp4_quantize(long blocks, bool wide, const void* x, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(long blocks, bool wide, const uint8_t* codes, const uint8_t* scales, void* out,
+                                   hipStream_t stream);
+
+// Balance loss (balance.hip) over S sequences; `off` and `mask` may be null.
+size_t balance_workspace_bytes(const Shape& s, int S);
+hipError_t launch_balance_loss(const Shape& s, const float* logits, const int32_t* idx, int S, const int32_t* off,
+                               const uint8_t* mask, float* loss, int32_t* count, int32_t* ntok, float* prob, void* ws,
+                               hipStream_t stream);
+hipError_t launch_balance_grad(const Shape& s, const float* logits, int S, const int32_t* off, const uint8_t* mask,
+                               const int32_t* count, const int32_t* ntok, const float* grad_loss, float* grad,
+                               hipStream_t stream);
+
+// Experts' products (experts.hip).  cap = 0: receive rows packed by expert
+// and `list` the E + 1 offsets; else `cap` rows per expert and `list` the
+// counts.  gate: 2 N weight rows and the gated activation; mx_out: its result
+// as MXFP4 (codes y, scales ys), else bf16.
+hipError_t launch_expert_product(const Shape& s, int cap, bool fp8, bool gate, bool mx_out, int K, int N,
+                                 const uint8_t* x, const void* xs, const int32_t* list, const uint8_t* w,
+                                 const uint8_t* ws, void* y, uint8_t* ys, hipStream_t stream);
+
 // Grid of the row kernels (dispatch, combine): one-wave workgroups, each
 // taking one 64-lane piece of a token's row (`segs` pieces per row) per
 // iteration; the grid is capped and the workgroups stride over the T * segs

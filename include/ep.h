@@ -349,6 +349,132 @@ EP_API int ep_combine_rank_partial(const ep_config_t* cfg, const void* y, const 
 EP_API int ep_combine_ranks(const ep_config_t* cfg, const void* partial, const int32_t* rank_slot, void* out,
                             void* stream);
 
+/* Element types of the calls below (the first two are EP_RECV_*'s values). */
+#define EP_TYPE_FP8_E4M3 0  /* e4m3 codes, fp32 scale per 128 columns        */
+#define EP_TYPE_BF16     1
+#define EP_TYPE_MXFP4    2  /* e2m1 codes, e8m0 scale per 32 columns         */
+#define EP_TYPE_FP32     3
+
+/* MXFP4 rows (OCP Microscaling Formats specification v1.0): every 32
+ * consecutive columns share one E8M0 scale 2^(b - 127), b one byte (255: the
+ * 32 values are NaN); the elements are E2M1 codes (sign, two exponent bits,
+ * one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a
+ * byte, the even column in the low four bits.  A row of C columns is C/2
+ * bytes of codes and, in an array of its own, C/32 bytes of scales.
+ *
+ * Quantise.  Per block: b = clamp(floor(log2 amax) - 2, -127, 127) + 127
+ * with amax the largest magnitude (b = 0 for a block of zeros); code =
+ * e2m1(x / 2^(b - 127)), rounded to nearest, ties to the even code, saturated
+ * to +-6.  A block with a NaN or an infinity gets b = 255 and codes 0.
+ *   rows, cols  rows >= 0; cols a multiple of 32, 32 <= cols <= 2^20
+ *   x_type      EP_TYPE_BF16 or EP_TYPE_FP32
+ *   x           device, [rows, cols], 16-byte aligned
+ *   codes       device, [rows, cols/2] bytes out, 16-byte aligned
+ *   scales      device, [rows, cols/32] bytes out
+ * Expert weights [E, N, K] are E * N rows of K columns. */
+EP_API int ep_mxfp4_quantize(int64_t rows, int32_t cols, int x_type, const void* x, void* codes, uint8_t* scales,
+                             void* stream);
+
+/* The values that MXFP4 rows stand for (exact in both types; bf16 and fp32
+ * overflow to infinity alike for scales beyond 2^125).
+ *   out_type  EP_TYPE_BF16 or EP_TYPE_FP32
+ *   out       device, [rows, cols] out, 16-byte aligned
+ * Other arguments and alignment as for ep_mxfp4_quantize. */
+EP_API int ep_mxfp4_dequantize(int64_t rows, int32_t cols, const void* codes, const uint8_t* scales, int out_type,
+                               void* out, void* stream);
+
+/* The experts' product, between dispatch and combine:
+ *   y[r, n] = bf16_rne( sum_k x[r, k] * w[e(r)][n, k] ),  sums in fp32,
+ * for every receive row r of expert e(r), i.e. r in [expert_offset[e],
+ * expert_offset[e + 1]); other rows of y are not written.  Every step takes
+ * the codes' values exactly; with EP_TYPE_FP8_E4M3 the sum over each 128
+ * columns is multiplied by the row's fp32 scale and added up.
+ *   x_type         EP_TYPE_FP8_E4M3 (ep_dispatch's payload) or EP_TYPE_MXFP4
+ *   in_features    K, a multiple of 128, 128 <= K <= 32768
+ *   out_features   N, a multiple of 32, 32 <= N <= 32768
+ *   x              device, [T*k, K] e4m3 codes or [T*k, K/2] bytes of MXFP4
+ *                  codes, 16-byte aligned, in ep_get_layout's receive rows
+ *   x_scales       device, fp32 [T*k, K/128] or bytes [T*k, K/32], 4-byte
+ *                  aligned
+ *   expert_offset  device, int32 [E + 1] from ep_get_layout (entries are
+ *                  clamped to [0, T*k]; it must not descend)
+ *   w              device, MXFP4 codes [E, N, K/2], 16-byte aligned
+ *   w_scales       device, bytes [E, N, K/32]
+ *   y              device, bf16 [T*k, N] out, 16-byte aligned
+ * cfg gives T, k and E; its hidden size takes no part.  The host does not wait
+ * for the counts.  Deterministic. */
+EP_API int ep_expert_product(const ep_config_t* cfg, int x_type, int32_t in_features, int32_t out_features,
+                             const void* x, const void* x_scales, const int32_t* expert_offset, const void* w,
+                             const uint8_t* w_scales, void* y, void* stream);
+
+/* The same over ep_dispatch_ll's receive rows: expert e's rows are
+ * [e*capacity, e*capacity + min(recv_count[e], capacity)).
+ *   x, x_scales, y  as above with E*capacity rows
+ *   recv_count      device, int32 [E] from ep_dispatch_ll (T*k in all at most) */
+EP_API int ep_expert_product_ll(const ep_config_t* cfg, int32_t capacity, int x_type, int32_t in_features,
+                                int32_t out_features, const void* x, const void* x_scales, const int32_t* recv_count,
+                                const void* w, const uint8_t* w_scales, void* y, void* stream);
+
+/* The gated product: w has 2 N rows per expert, N gate rows and then N up
+ * rows, and with a, b the two sums of column n (fp32)
+ *   h[r, n] = a / (1 + exp(-a)) * b.
+ *   y_type    EP_TYPE_BF16: h rounded once, y [T*k, N] (y_scales NULL);
+ *             EP_TYPE_MXFP4: h quantised as by ep_mxfp4_quantize from fp32,
+ *             y [T*k, N/2] bytes, y_scales [T*k, N/32] bytes: the rows of the
+ *             next product
+ *   w         device, MXFP4 codes [E, 2N, K/2]; w_scales [E, 2N, K/32]
+ * Other arguments as for ep_expert_product; N up to 16384. */
+EP_API int ep_expert_swiglu(const ep_config_t* cfg, int x_type, int32_t in_features, int32_t out_features,
+                            const void* x, const void* x_scales, const int32_t* expert_offset, const void* w,
+                            const uint8_t* w_scales, int y_type, void* y, uint8_t* y_scales, void* stream);
+
+EP_API int ep_expert_swiglu_ll(const ep_config_t* cfg, int32_t capacity, int x_type, int32_t in_features,
+                               int32_t out_features, const void* x, const void* x_scales, const int32_t* recv_count,
+                               const void* w, const uint8_t* w_scales, int y_type, void* y, uint8_t* y_scales,
+                               void* stream);
+
+/* Balance loss of the router with its per-expert counts, by sequence.  Over
+ * the n counted tokens t of sequence s (seq_offset[s] <= t <
+ * seq_offset[s + 1] and token_mask[t] != 0), with s[t,e] the gate's scores
+ * (ep_scores) and p[t,e] = s[t,e] / sum_j s[t,j] (0 where that sum is 0):
+ *   count[s,e] = picks of e among topk_idx[t, :]   (out-of-range picks not
+ *                counted, a repeated pick each time)
+ *   prob[s,e]  = (1/n) sum_t p[t,e]
+ *   loss[s]    = sum_e E * count[s,e] / (k n) * prob[s,e]
+ * and all of them 0 where n = 0.  Tokens that are not counted take no part,
+ * whatever their logits hold.
+ *   logits      device, fp32 [T, E]
+ *   topk_idx    device, int32 [T, k]
+ *   num_seqs    S, 1 <= S <= 65536
+ *   seq_offset  device, int32 [S + 1], ascending from 0 to T (entries are
+ *               clamped to [0, T]), or NULL: one sequence (S = 1)
+ *   token_mask  device, bytes [T], or NULL: every token counts
+ *   loss        device, fp32 [S] out
+ *   count       device, int32 [S, E] out
+ *   ntok        device, int32 [S] out: n
+ *   prob        device, fp32 [S, E] out
+ *   workspace   device, >= ep_balance_workspace_bytes(cfg, S) bytes, 256-byte
+ *               aligned; scratch after the call
+ * Sums over tokens: fp32 runs of at most 32, then longer; across the batch in
+ * double.  Deterministic.  Alignment: 4 bytes. */
+EP_API size_t ep_balance_workspace_bytes(const ep_config_t* cfg, int32_t num_seqs);
+EP_API int ep_balance_loss(const ep_config_t* cfg, const float* logits, const int32_t* topk_idx, int32_t num_seqs,
+                           const int32_t* seq_offset, const uint8_t* token_mask, float* loss, int32_t* count,
+                           int32_t* ntok, float* prob, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of sum_s grad_loss[s] * loss[s] with respect to the logits, the
+ * counts taken as constants.  With c[e] = E count[s,e] / (k n^2):
+ *   grad_logits[t,e] = grad_loss[s] * (c[e] - sum_j c[j] p[t,j]) * p[t,e] * (1 - s[t,e])
+ * and 0 for tokens that are not counted or in no sequence.
+ *   count, ntok  device, from ep_balance_loss
+ *   grad_loss    device, fp32 [S]
+ *   grad_logits  device, fp32 [T, E] out (may alias logits)
+ * Other arguments as for ep_balance_loss; no workspace. */
+EP_API int ep_balance_loss_backward(const ep_config_t* cfg, const float* logits, const int32_t* count,
+                                    const int32_t* ntok, int32_t num_seqs, const int32_t* seq_offset,
+                                    const uint8_t* token_mask, const float* grad_loss, float* grad_logits,
+                                    void* stream);
+
 /* CU budget ([GH#6] "Technical Overview of DeepEP": SM-count control; [DAY2]
  * "All-to-All通信": communication kernels confined to a few SMs and
  * overlapped with the compute stream).  Creates a HIP stream whose kernels
