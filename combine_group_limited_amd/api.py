@@ -469,8 +469,8 @@ def _experts(cfg: Config, capacity, x, x_scales, w, w_scales, rows_of, gate: boo
     dev = x.device
     nrows = cfg.nrows if capacity is None else cfg.E * capacity
     _want(w, "w", (cfg.E,) + tuple(w.shape[1:]), torch.uint8, dev)
-    if w.dim() != 3 or not w.shape[2] or w.shape[2] % 64 or (gate and w.shape[1] % 2):
-        raise ValueError("w must be [E, %s, K/2] bytes, K a multiple of 128" % ("2 * N" if gate else "N"))
+    if w.dim() != 3 or not w.shape[2] or w.shape[2] % 16 or (gate and w.shape[1] % 2):
+        raise ValueError("w must be [E, %s, K/2] bytes, K a multiple of 32" % ("2 * N" if gate else "N"))
     K, N = 2 * w.shape[2], w.shape[1] // 2 if gate else w.shape[1]
     _want(w_scales, "w_scales", (cfg.E, w.shape[1], K // 32), torch.uint8, dev)
     fp8 = x_scales.dtype == torch.float32

@@ -126,13 +126,15 @@ int expert_product(const ep_config_t* cfg, int32_t capacity, int x_type, int32_t
                    int y_type, void* y, uint8_t* y_scales, void* stream) {
     if (x_type != EP_TYPE_FP8_E4M3 && x_type != EP_TYPE_MXFP4) return EP_ERR_INVALID_ARG;
     if (y_type != EP_TYPE_BF16 && y_type != EP_TYPE_MXFP4) return EP_ERR_INVALID_ARG;
-    if (K < 128 || K % 128 != 0 || N < 32 || N % 32 != 0) return EP_ERR_INVALID_ARG;
+    const int unit = x_type == EP_TYPE_FP8_E4M3 ? 128 : 32;  // columns of a scale
+    if (K < unit || K % unit != 0 || N < 32 || N % 32 != 0) return EP_ERR_INVALID_ARG;
     const bool mx_out = y_type == EP_TYPE_MXFP4;
     if (!mx_out && y_scales) return EP_ERR_INVALID_ARG;
     if (K > kMaxFeatures || N > (gate ? kMaxFeatures / 2 : kMaxFeatures)) return EP_ERR_UNSUPPORTED;
     if (!list || !w || !w_scales) return EP_ERR_INVALID_ARG;
     if (cfg->num_tokens > 0 && (!x || !x_scales || !y || (mx_out && !y_scales))) return EP_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(x_scales, 4) || !aligned(list, 4) || !aligned(w, 16) || !aligned(y, 16))
+    if (!aligned(x, 16) || !aligned(x_scales, 4) || !aligned(list, 4) || !aligned(w, 16) ||
+        !aligned(w_scales, 4) || !aligned(y, 16))
         return EP_ERR_ALIGNMENT;
     return hip_status(ep::launch_expert_product(
         shape_of(cfg), capacity, x_type == EP_TYPE_FP8_E4M3, gate, mx_out, K, N, static_cast<const uint8_t*>(x),

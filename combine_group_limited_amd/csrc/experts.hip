@@ -50,6 +50,13 @@ constexpr int kUnit = 127;         // E8M0 scale of 1
 
 enum Epilogue { kPlain, kGated, kGatedMx };
 
+// a constant as a function argument
+template <int I>
+struct Int {
+    static constexpr int value = I;
+    __device__ constexpr operator int() const { return I; }
+};
+
 // Output columns of a wavefront's kNT weight tiles.
 template <int EPI>
 constexpr int kCols = EPI == kPlain ? 16 * kNT : 8 * kNT;
@@ -78,13 +85,13 @@ __device__ __forceinline__ i32x8 operand(const XPiece<FP8>& p) {
     else return i32x8{p.v[0].x, p.v[0].y, p.v[0].z, p.v[0].w, 0, 0, 0, 0};
 }
 
-// c + w x, 16 weight rows by 16 activation rows over 128 columns; XB is the
-// byte of `xs` that holds the activations' scale.
-template <bool FP8, int XB>
+// c + w x, 16 weight rows by 16 activation rows over 128 columns; WB and XB are
+// the bytes of `ws` and `xs` that hold the scales.
+template <bool FP8, int WB, int XB>
 __device__ __forceinline__ f32x4 multiply(i32x4 w, int ws, const XPiece<FP8>& x, int xs, f32x4 c) {
     const i32x8 a = {w.x, w.y, w.z, w.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, operand<FP8>(x), c, kFp4, FP8 ? kFp8 : kFp4, 0, ws, XB,
-                                                            xs);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, operand<FP8>(x), c, kFp4, FP8 ? kFp8 : kFp4, WB, ws,
+                                                            XB, xs);
 }
 
 // Row of the weights that lane row `a` (0 .. 15) of tile 0 loads, for output
@@ -101,6 +108,10 @@ __device__ __forceinline__ int tile_rows(int i, int N) {
 // Byte offset that lies outside every buffer resource here (all are below
 // 2^31 bytes).
 constexpr int kOutside = (int)0x80000000;
+
+// `at` where i < n, else outside every resource, without a branch (one would
+// split the loops below, and matrix instructions would move past it).
+__device__ __forceinline__ int offset_if(int at, int i, int n) { return at | (((n - 1 - i) >> 31) & kOutside); }
 
 // gate * sigmoid(gate) * up.  The hardware exponential and reciprocal are good
 // to about a unit in the 22nd bit here; the result is rounded to 8 bits or
@@ -150,12 +161,15 @@ __device__ __forceinline__ bool find_tile(const Rows& rows, uint32_t ntiles, uin
     const int lane = threadIdx.x & 63, run = (rows.E + kWave - 1) / kWave;
     const auto tiles_of = [&](int e) { return (rows.count(e) + BM - 1) / BM; };
     int mine = 0;
+    const auto add = [&](auto first, auto last) {
+        int n[decltype(last)::value];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mine += i < run ? tiles_of(lane * run + i) : 0;
-    if (run > 4) {
+        for (int i = first; i < last; ++i) n[i] = tiles_of(lane * run + i);
 #pragma unroll
-        for (int i = 4; i < kMost; ++i) mine += i < run ? tiles_of(lane * run + i) : 0;
-    }
+        for (int i = first; i < last; ++i) mine += i < run ? n[i] : 0;
+    };
+    add(Int<0>(), Int<4>());
+    if (run > 4) add(Int<4>(), Int<kMost>());
     int upto = wave_inclusive_sum(mine);
     const uint32_t n = (uint32_t)__builtin_amdgcn_readlane(upto, 63) * ntiles;
     if (v >= n) return false;
@@ -205,10 +219,10 @@ struct Sources {
     }
 };
 
-// E8M0 scale of a block of 32 whose largest magnitude is `amax` (quant.hip's
-// rule) and the codes of four values under it.
-__device__ __forceinline__ uint32_t mx_scale(float amax_bits) {
-    const uint32_t f = __float_as_uint(amax_bits) >> 23;
+// E8M0 scale of a block of 32 whose largest magnitude has the bits `amax`
+// (quant.hip's rule) and the codes of four values under it.
+__device__ __forceinline__ uint32_t mx_scale(uint32_t amax) {
+    const uint32_t f = amax >> 23;
     return f == 255u ? 255u : (f > 2u ? f - 2u : 0u);
 }
 
@@ -234,7 +248,7 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
     __shared__ f32x4 part[KS][MT * kNT][kWave];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, m = lane & 15;
-    const int K = p.K, N = p.N, steps = K / kStep;
+    const int K = p.K, N = p.N, steps = (K + kStep - 1) / kStep, blocks = K / 32;
 
     struct Piece {
         i32x4 w[STEPS][kNT];
@@ -260,26 +274,30 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
             xat[j] = row * (FP8 ? K : K / 2) + g * 16;
             xsat[j] = FP8 ? row * (K / 32) : row * (K / 32) + g;
         }
+        // past the last step (and the last block of MXFP4 rows) these read zeros
         const auto load = [&](Piece& q, int step0) {
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                const int step = min(step0 + s, steps - 1);
+                const int step = step0 + s, b = step * 4 + g;
+                const int wto = offset_if(wat, b, blocks), wsto = offset_if(wsat, b, blocks);
 #pragma unroll
                 for (int i = 0; i < kNT; ++i) {
-                    q.w[s][i] = __builtin_amdgcn_raw_buffer_load_b128(src.w, wat, tile_rows<EPI>(i, N) * (K / 2) + step * 64,
-                                                                   kCached);
-                    q.ws[s][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.ws, wsat, tile_rows<EPI>(i, N) * (K / 32) + step * 4,
-                                                                      kCached);
+                    const int row = tile_rows<EPI>(i, N);
+                    q.w[s][i] = __builtin_amdgcn_raw_buffer_load_b128(src.w, wto, row * (K / 2) + step * 64, kCached);
+                    q.ws[s][i] =
+                        (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.ws, wsto, row * blocks + step * 4, kCached);
                 }
 #pragma unroll
                 for (int j = 0; j < MT; ++j) {
+                    const int xto = offset_if(xat[j], b, blocks), xsto = offset_if(xsat[j], b, blocks);
+                    q.x[s][j].v[0] =
+                        __builtin_amdgcn_raw_buffer_load_b128(src.x, xto, step * (FP8 ? 128 : 64), kCached);
                     if constexpr (FP8) {
-                        q.x[s][j].v[0] = __builtin_amdgcn_raw_buffer_load_b128(src.x, xat[j], step * 128, kCached);
-                        q.x[s][j].v[1] = __builtin_amdgcn_raw_buffer_load_b128(src.x, xat[j] + 64, step * 128, kCached);
-                        q.xs[s][j] = __builtin_amdgcn_raw_buffer_load_b32(src.xs, xsat[j], step * 4, kCached);
+                        q.x[s][j].v[1] =
+                            __builtin_amdgcn_raw_buffer_load_b128(src.x, xto + 64, step * 128, kCached);
+                        q.xs[s][j] = __builtin_amdgcn_raw_buffer_load_b32(src.xs, xsto, step * 4, kCached);
                     } else {
-                        q.x[s][j].v[0] = __builtin_amdgcn_raw_buffer_load_b128(src.x, xat[j], step * 64, kCached);
-                        q.xs[s][j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.xs, xsat[j], step * 4, kCached);
+                        q.xs[s][j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.xs, xsto, step * 4, kCached);
                     }
                 }
             }
@@ -290,10 +308,9 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
         for (int j = 0; j < MT; ++j)
 #pragma unroll
             for (int i = 0; i < kNT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const auto use = [&](const Piece& q, int step0) {
+        const auto use = [&](const Piece& q) {
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                if (step0 + s >= steps) break;
 #pragma unroll
                 for (int j = 0; j < MT; ++j) {
                     XPiece<FP8> high, low;
@@ -308,13 +325,13 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
                     for (int i = 0; i < kNT; ++i) {
                         if constexpr (FP8) {
                             f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
-                            r = multiply<true, 0>(q.w[s][i], q.ws[s][i], low, kUnit, r);
-                            r = multiply<true, 0>(q.w[s][i], q.ws[s][i], high, kUnit, r);
+                            r = multiply<true, 0, 0>(q.w[s][i], q.ws[s][i], low, kUnit, r);
+                            r = multiply<true, 0, 0>(q.w[s][i], q.ws[s][i], high, kUnit, r);
                             const float sc = __int_as_float(q.xs[s][j]);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) acc[j][i][c] = __builtin_fmaf(sc, r[c], acc[j][i][c]);
                         } else {
-                            acc[j][i] = multiply<false, 0>(q.w[s][i], q.ws[s][i], q.x[s][j], q.xs[s][j], acc[j][i]);
+                            acc[j][i] = multiply<false, 0, 0>(q.w[s][i], q.ws[s][i], q.x[s][j], q.xs[s][j], acc[j][i]);
                         }
                     }
                 }
@@ -322,16 +339,12 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
         };
         constexpr int kRun = KS * STEPS;
         Piece a, b;
-        int at = wave * STEPS;
-        if (at < steps) load(a, at);
-        while (at < steps) {
-            if (at + kRun < steps) load(b, at + kRun);
-            use(a, at);
-            at += kRun;
-            if (at >= steps) break;
-            if (at + kRun < steps) load(a, at + kRun);
-            use(b, at);
-            at += kRun;
+        load(a, wave * STEPS);
+        for (int at = wave * STEPS; at < steps; at += 2 * kRun) {
+            load(b, at + kRun);
+            use(a);
+            load(a, at + 2 * kRun);
+            use(b);
         }
 
 #pragma unroll
@@ -377,7 +390,7 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
                 a = max(a, dpp_u32<kDppXor1>(a));
                 a = max(a, dpp_u32<kDppXor2>(a));
                 a = max(a, dpp_u32<kDppHalfMirror>(a));
-                const uint32_t s = mx_scale(__uint_as_float(a));
+                const uint32_t s = mx_scale(a);
                 if (on) {
                     *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.y) + (yrow * N + n) / 2) =
                         (uint16_t)mx_codes4(o[0], o[1], o[2], o[3], s);
@@ -390,29 +403,27 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
 
 // ------------------------------------------------- many rows per expert
 
-// A workgroup takes 2 x MT x 16 rows by 4 x kCols columns with 2 x 4
-// wavefronts, each MT x 16 rows by kCols columns.  The rows of a 128-column step go through LDS
-// (double buffered, loaded two steps ahead); a wavefront's weights go straight
-// to registers, one step ahead.  Row tiles without rows are skipped, four at a
-// time.
-constexpr int kWavesM = 2, kWavesN = 4, kThreads = 64 * kWavesM * kWavesN;
-template <bool FP8>
-constexpr int kTileMT = FP8 ? 4 : 8;
-template <bool FP8>
-constexpr int kTileBM = kWavesM * 16 * kTileMT<FP8>;
+// A workgroup takes 128 rows by 8 x kCols columns with 8 wavefronts side by
+// side, each all 128 rows by kCols columns.  The rows of a 128-column step go
+// through LDS (two buffers), as do the weights' scales of four steps at a
+// time, turned so that a lane reads its four tiles' bytes at once; a
+// wavefront's weights are its own and go straight to registers, several steps
+// ahead.  Every step has one barrier.  Tiles of up to 64 rows multiply only half.
+constexpr int kTileWaves = 8, kTileMT = 8, kTileRows = 16 * kTileMT, kTileThreads = 64 * kTileWaves;
 
 template <bool FP8, int EPI>
-__global__ __launch_bounds__(kThreads, 1) void tile_kernel(Product p, int ntiles) {
-    constexpr int kMT = kTileMT<FP8>, kTileRows = kTileBM<FP8>, kHalf = kTileRows / kWavesM;
-    constexpr int kChunks = FP8 ? 8 : 4;                            // 16-byte chunks of a row's step
-    constexpr int kPer = kTileRows * kChunks / kThreads;            // chunks staged by a thread
-    constexpr int kParts = FP8 ? 2 : 1;                             // FP8: low codes, then high codes
+__global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p, int ntiles) {
+    constexpr int kMT = kTileMT;
+    constexpr int kChunks = FP8 ? 8 : 4;                         // 16-byte chunks of a row's step
+    constexpr int kPer = kTileRows * kChunks / kTileThreads;     // chunks staged by a thread
+    constexpr int kParts = FP8 ? 2 : 1;                          // FP8: low codes, then high codes
+    constexpr int kWSets = 2, kXSets = FP8 ? 1 : 2;    // steps of weights and rows in registers
     __shared__ i32x4 rows_lds[2][kParts][kTileRows * kChunks];
-    __shared__ __align__(16) uint8_t scale_lds[2][kTileRows * 4];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ __align__(16) uint8_t xs_lds[2][kTileRows * 4];
+    __shared__ __align__(16) uint8_t ws_lds[2][4][kTileThreads * 4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, m = lane & 15;
-    const int wm = wave / kWavesN, wn = wave % kWavesN;
-    const int K = p.K, N = p.N, steps = K / kStep;
+    const int K = p.K, N = p.N, steps = (K + kStep - 1) / kStep, blocks = K / 32;
 
     // 16-byte chunk c of row r lies at a place of its own in the row, so that
     // the eight rows read together fall into different banks
@@ -423,190 +434,234 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(Product p, int ntiles
 
     Tile t;
     if (!find_tile<kTileRows>(p.rows, ntiles, blockIdx.x, t)) return;
-    {
-        const Sources<FP8, EPI> src(p, t);
-        const int n0 = (t.n * kWavesN + wn) * kCols<EPI>;
-        const bool columns = n0 < N;
-        const int mine = t.rows - wm * kHalf;  // rows of this wavefront
-        const int wrow = weight_row<EPI>(n0, m);
-        const int wat = wrow < N ? wrow * (K / 2) + g * 16 : kOutside;
-        const int wsat = wrow < N ? wrow * (K / 32) + g : kOutside;
-        // a thread stages chunk threadIdx.x and those kStride rows apart
-        constexpr int kStride = kThreads / kChunks;
-        const int xrow = threadIdx.x / kChunks, xbytes = FP8 ? K : K / 2;
-        const int xat = xrow * xbytes + threadIdx.x % kChunks * 16;
-        const int xto = place(xrow, threadIdx.x % kChunks);
-        const int srow = threadIdx.x & (kTileRows - 1);
-        const int sat = srow * (K / 32);  // a step's scales: 4 bytes of a row in both forms
+    const Sources<FP8, EPI> src(p, t);
+    const int n0 = (t.n * kTileWaves + wave) * kCols<EPI>;
 
-        struct Staged {
-            i32x4 x[kPer];
-            int xs;
-        };
-        struct Weights {
-            i32x4 w[kNT];
-            int ws[kNT];
-        };
-        const auto load_rows = [&](Staged& q, int step) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                q.x[j] = __builtin_amdgcn_raw_buffer_load_b128(src.x, xat + j * kStride * xbytes, step * (FP8 ? 128 : 64),
-                                                             kCached);
-            q.xs = __builtin_amdgcn_raw_buffer_load_b32(src.xs, sat, step * 4, kCached);
-        };
-        const auto store_rows = [&](const Staged& q, int buf) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int to = xto + j * kStride * kChunks;
-                if constexpr (FP8) {
-                    const i32x4 high = upper_codes(q.x[j]);
-                    rows_lds[buf][0][to] = q.x[j] ^ high;
-                    rows_lds[buf][kParts - 1][to] = high;
-                } else {
-                    rows_lds[buf][0][to] = q.x[j];
-                }
-            }
-            if (threadIdx.x < kTileRows) {
-                // row 16 (MT h + i) + c: the MT rows i that lane c of half h reads lie together
-                const int at = srow / kHalf * kHalf + (srow & 15) * kMT + (srow >> 4) % kMT;
-                if constexpr (FP8) {
-                    *reinterpret_cast<int*>(&scale_lds[buf][at * 4]) = q.xs;
-                } else {
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) scale_lds[buf][b * kTileRows + at] = (uint8_t)(q.xs >> (8 * b));
-                }
-            }
-        };
-        const auto load_weights = [&](Weights& q, int step) {
-#pragma unroll
-            for (int i = 0; i < kNT; ++i) {
-                q.w[i] = __builtin_amdgcn_raw_buffer_load_b128(src.w, wat, tile_rows<EPI>(i, N) * (K / 2) + step * 64,
-                                                                   kCached);
-                q.ws[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.ws, wsat, tile_rows<EPI>(i, N) * (K / 32) + step * 4,
-                                                                      kCached);
-            }
-        };
+    // this lane's weights
+    const int wrow = weight_row<EPI>(n0, m);
+    const int wat = wrow < N ? wrow * (K / 2) + g * 16 : kOutside;
+    // this thread's chunks of the rows: chunk tid and those kStride rows apart
+    constexpr int kStride = kTileThreads / kChunks;
+    const int xrow = tid / kChunks, xbytes = FP8 ? K : K / 2;
+    const int xat = xrow * xbytes + tid % kChunks * 16;
+    const int xto = place(xrow, tid % kChunks);
+    // its row scale: FP8 one of a row (four threads the same), MXFP4 one byte;
+    // row 16 i + c lies at 8 c + i, where the lanes c read their eight rows
+    const int srow = tid >> 2, sto = (srow & 15) * 8 + (srow >> 4);
+    // its weight row's scales: tile i, lane row a of this wavefront's tiles
+    const int vtile = lane >> 4, vrow = weight_row<EPI>(n0, m) + tile_rows<EPI>(vtile, N);
+    const int vat = wrow < N ? vrow * blocks : kOutside;
+    const int vshift = vat & 3;  // rows of scales need not be a multiple of 4 bytes
 
-        f32x4 acc[kMT][kNT];
+    struct Staged {
+        i32x4 x[kPer];
+        int xs;
+    };
+    struct Scales {
+        i32x4 v;
+        int more;
+    };
+    const auto load_rows = [&](Staged& q, int step) {
+        const int i = FP8 ? step : step * 4 + (tid & 3), n = FP8 ? steps : blocks;
 #pragma unroll
-        for (int j = 0; j < kMT; ++j)
-#pragma unroll
-            for (int i = 0; i < kNT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-        constexpr int kHold = FP8 ? 2 : 4;  // row tiles read from LDS at a time
-        const int rx0 = place(wm * kHalf + m, g), rx1 = place(wm * kHalf + m, FP8 ? g + 4 : g);
-        const auto compute = [&](const Weights& q, int buf) {
-#pragma unroll
-            for (int h = 0; h < kMT; h += kHold) {
-                if (h * 16 >= mine) break;
-                XPiece<FP8> x[kHold], high[kHold];
-#pragma unroll
-                for (int j = 0; j < kHold; ++j) {
-                    x[j].v[0] = rows_lds[buf][0][rx0 + (h + j) * 16 * kChunks];
-                    if constexpr (FP8) {
-                        x[j].v[1] = rows_lds[buf][0][rx1 + (h + j) * 16 * kChunks];
-                        high[j].v[0] = rows_lds[buf][kParts - 1][rx0 + (h + j) * 16 * kChunks];
-                        high[j].v[1] = rows_lds[buf][kParts - 1][rx1 + (h + j) * 16 * kChunks];
-                    }
-                }
-                if constexpr (FP8) {
-                    const float2 sc = *reinterpret_cast<const float2*>(&scale_lds[buf][(wm * kHalf + m * kMT + h) * 4]);
-#pragma unroll
-                    for (int j = 0; j < kHold; ++j)
-#pragma unroll
-                        for (int i = 0; i < kNT; ++i) {
-                            f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
-                            r = multiply<true, 0>(q.w[i], q.ws[i], x[j], kUnit, r);
-                            r = multiply<true, 0>(q.w[i], q.ws[i], high[j], kUnit, r);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                acc[h + j][i][c] = __builtin_fmaf(j ? sc.y : sc.x, r[c], acc[h + j][i][c]);
-                        }
-                } else {
-                    const int sc =
-                        *reinterpret_cast<const int*>(&scale_lds[buf][g * kTileRows + wm * kHalf + m * kMT + h]);
-#pragma unroll
-                    for (int i = 0; i < kNT; ++i) {
-                        acc[h + 0][i] = multiply<false, 0>(q.w[i], q.ws[i], x[0], sc, acc[h + 0][i]);
-                        acc[h + 1][i] = multiply<false, 1>(q.w[i], q.ws[i], x[1], sc, acc[h + 1][i]);
-                        acc[h + 2][i] = multiply<false, 2>(q.w[i], q.ws[i], x[2], sc, acc[h + 2][i]);
-                        acc[h + 3][i] = multiply<false, 3>(q.w[i], q.ws[i], x[3], sc, acc[h + 3][i]);
-                    }
-                }
-            }
-        };
-
-        Staged st;
-        Weights wa, wb;
-        load_rows(st, 0);
-        load_weights(wa, 0);
-        store_rows(st, 0);
-        if (steps > 1) load_rows(st, 1);
-        // step s: its rows are in buffer s % 2 when every wavefront is past the
-        // barrier, and the other buffer is no longer read
-        const auto body = [&](int s, const Weights& now, Weights& next) {
-            __syncthreads();
-            if (s + 1 < steps) {
-                store_rows(st, (s + 1) & 1);
-                load_weights(next, s + 1);
-                if (s + 2 < steps) load_rows(st, s + 2);
-            }
-            if (columns) compute(now, s & 1);
-        };
-        for (int s = 0; s < steps; s += 2) {
-            body(s, wa, wb);
-            if (s + 1 < steps) body(s + 1, wb, wa);
+        for (int j = 0; j < kPer; ++j) {
+            const int at = offset_if(xat + j * kStride * xbytes, i, n);
+            q.x[j] = __builtin_amdgcn_raw_buffer_load_b128(src.x, at, step * (FP8 ? 128 : 64), kCached);
         }
+        if constexpr (FP8) {
+            q.xs = __builtin_amdgcn_raw_buffer_load_b32(src.xs, offset_if(srow * blocks, i, n), step * 4, kCached);
+        } else {
+            const int at = offset_if(srow * blocks + (tid & 3), i, n);
+            q.xs = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.xs, at, step * 4, kCached);
+        }
+    };
+    const auto store_rows = [&](const Staged& q, int buf) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int to = xto + j * kStride * kChunks;
+            if constexpr (FP8) {
+                const i32x4 high = upper_codes(q.x[j]);
+                rows_lds[buf][0][to] = q.x[j] ^ high;
+                rows_lds[buf][kParts - 1][to] = high;
+            } else {
+                rows_lds[buf][0][to] = q.x[j];
+            }
+        }
+        if constexpr (FP8) *reinterpret_cast<int*>(&xs_lds[buf][sto * 4]) = q.xs;
+        else xs_lds[buf][(tid & 3) * kTileRows + sto] = (uint8_t)q.xs;
+    };
+    const auto load_weights = [&](i32x4 (&w)[kNT], int step) {
+        const int at = offset_if(wat, step * 4 + g, blocks);
+#pragma unroll
+        for (int i = 0; i < kNT; ++i)
+            w[i] = __builtin_amdgcn_raw_buffer_load_b128(src.w, at, tile_rows<EPI>(i, N) * (K / 2) + step * 64,
+                                                         kCached);
+    };
+    // the scales of steps 4 four .. 4 four + 3: 16 bytes of a row, from the
+    // aligned words that hold them
+    const auto load_scales = [&](Scales& q, int four) {
+        const int at = offset_if(vat - vshift, four * 16, blocks);
+        q.v = __builtin_amdgcn_raw_buffer_load_b128(src.ws, at, four * 16, kCached);
+        q.more = __builtin_amdgcn_raw_buffer_load_b32(src.ws, offset_if(at + 16, 0, vshift), four * 16, kCached);
+    };
+    const auto store_scales = [&](const Scales& q, int four) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint32_t lo = (uint32_t)q.v[s], hi = (uint32_t)(s < 3 ? q.v[s < 3 ? s + 1 : 3] : q.more);
+            const uint32_t d = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)vshift);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const bool in = four * 16 + s * 4 + b < blocks;  // bytes past the row are another row's
+                ws_lds[four & 1][s][wave * 256 + (b * 16 + m) * 4 + vtile] = in ? (uint8_t)(d >> (8 * b)) : 0;
+            }
+        }
+    };
 
-        // the sums are final here, with every lane active (the matrix
-        // instructions must not move into the guarded stores below)
+    f32x4 acc[kMT][kNT];
 #pragma unroll
-        for (int j = 0; j < kMT; ++j)
+    for (int j = 0; j < kMT; ++j)
 #pragma unroll
-            for (int i = 0; i < kNT; ++i) asm volatile("" : "+v"(acc[j][i]));
+        for (int i = 0; i < kNT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-        // lane (g, m): row 16 j + m, consecutive columns
+    constexpr int kHold = FP8 ? 1 : 4;  // row tiles read from LDS at a time
+    const int rx0 = place(m, g), rx1 = place(m, FP8 ? g + 4 : g);
+    const auto compute = [&](auto halves, const i32x4 (&w)[kNT], int buf, int step) {
+        const int ws = *reinterpret_cast<const int*>(&ws_lds[(step >> 2) & 1][step & 3][wave * 256 + lane * 4]);
+        // row tiles H .. H + kHold - 1
+        const auto rows = [&](auto first) {
+            constexpr int H = decltype(first)::value;
+            XPiece<FP8> x[kHold], high[kHold];
 #pragma unroll
-        for (int j = 0; j < kMT; ++j) {
-            const int row = wm * kHalf + j * 16 + m;
-            const size_t yrow = (size_t)t.row0 + row;
-            if constexpr (EPI == kPlain) {
-                const int n = n0 + 16 * g;
-                if (row < t.rows && n < N) {
-                    i32x4* to = reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.y) + yrow * N + n);
+            for (int j = 0; j < kHold; ++j) {
+                x[j].v[0] = rows_lds[buf][0][rx0 + (H + j) * 16 * kChunks];
+                if constexpr (FP8) {
+                    x[j].v[1] = rows_lds[buf][0][rx1 + (H + j) * 16 * kChunks];
+                    high[j].v[0] = rows_lds[buf][kParts - 1][rx0 + (H + j) * 16 * kChunks];
+                    high[j].v[1] = rows_lds[buf][kParts - 1][rx1 + (H + j) * 16 * kChunks];
+                }
+            }
+            if constexpr (FP8) {
+                const float sc = *reinterpret_cast<const float*>(&xs_lds[buf][(m * kMT + H) * 4]);
+                f32x4 r[kNT];
+                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                r[0] = multiply<true, 0, 0>(w[0], ws, x[0], kUnit, zero);
+                r[1] = multiply<true, 1, 0>(w[1], ws, x[0], kUnit, zero);
+                r[2] = multiply<true, 2, 0>(w[2], ws, x[0], kUnit, zero);
+                r[3] = multiply<true, 3, 0>(w[3], ws, x[0], kUnit, zero);
+                r[0] = multiply<true, 0, 0>(w[0], ws, high[0], kUnit, r[0]);
+                r[1] = multiply<true, 1, 0>(w[1], ws, high[0], kUnit, r[1]);
+                r[2] = multiply<true, 2, 0>(w[2], ws, high[0], kUnit, r[2]);
+                r[3] = multiply<true, 3, 0>(w[3], ws, high[0], kUnit, r[3]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const f32x4 a = acc[j][2 * h], b = acc[j][2 * h + 1];
-                        to[h] = i32x4{(int)pack_bf16x2(a[0], a[1]), (int)pack_bf16x2(a[2], a[3]),
-                                      (int)pack_bf16x2(b[0], b[1]), (int)pack_bf16x2(b[2], b[3])};
-                    }
+                for (int i = 0; i < kNT; ++i) {
+                    const f32x4 o = acc[H][i];
+                    acc[H][i] = f32x4{__builtin_fmaf(sc, r[i][0], o[0]), __builtin_fmaf(sc, r[i][1], o[1]),
+                                      __builtin_fmaf(sc, r[i][2], o[2]), __builtin_fmaf(sc, r[i][3], o[3])};
                 }
             } else {
-                const int n = n0 + 8 * g;
-                f32x4 a, b;
+                const int sc = *reinterpret_cast<const int*>(&xs_lds[buf][g * kTileRows + m * kMT + H]);
+                const auto column = [&](auto i) {
+                    constexpr int I = decltype(i)::value;
+                    acc[H + 0][I] = multiply<false, I, 0>(w[I], ws, x[0], sc, acc[H + 0][I]);
+                    acc[H + 1][I] = multiply<false, I, 1>(w[I], ws, x[1 % kHold], sc, acc[H + 1][I]);
+                    acc[H + 2][I] = multiply<false, I, 2>(w[I], ws, x[2 % kHold], sc, acc[H + 2][I]);
+                    acc[H + 3][I] = multiply<false, I, 3>(w[I], ws, x[3 % kHold], sc, acc[H + 3][I]);
+                };
+                column(Int<0>()), column(Int<1>()), column(Int<2>()), column(Int<3>());
+            }
+        };
+        const auto half = [&](auto first) {
+            constexpr int H = decltype(first)::value;
+            rows(Int<H>());
+            if constexpr (kHold == 1) rows(Int<H + 1>()), rows(Int<H + 2>()), rows(Int<H + 3>());
+        };
+        half(Int<0>());
+        if constexpr (halves > 1) half(Int<4>());
+    };
+
+    Staged st[kXSets];
+    i32x4 w[kWSets][kNT];
+    Scales sc;
+    load_scales(sc, 0);
+    load_rows(st[0], 0);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    a[c] = gated(acc[j][0][c], acc[j][2][c]);
-                    b[c] = gated(acc[j][1][c], acc[j][3][c]);
-                }
-                if constexpr (EPI == kGated) {
-                    if (row < t.rows && n < N)
-                        *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.y) + yrow * N + n) =
-                            i32x4{(int)pack_bf16x2(a[0], a[1]), (int)pack_bf16x2(a[2], a[3]),
+    for (int i = 0; i + 1 < kWSets; ++i) load_weights(w[i], i);
+    store_scales(sc, 0);
+    store_rows(st[0], 0);
+#pragma unroll
+    for (int i = 1; i <= kXSets; ++i) load_rows(st[i % kXSets], i);
+    // Step s: its rows and scales are in LDS when every wavefront is past the
+    // barrier, and the other buffers are no longer read.  Four steps at a time,
+    // without conditions: loads past the last step read zeros, which add
+    // nothing, and each wait counts exactly what is in flight.
+    const auto loop = [&](auto halves) {
+        for (int s = 0; s < steps; s += 4) {
+            const auto body = [&](auto phase) {
+                constexpr int I = decltype(phase)::value;
+                __syncthreads();
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (I == 0) load_scales(sc, (s >> 2) + 1);
+                store_rows(st[(I + 1) % kXSets], (I + 1) & 1);
+                load_rows(st[(I + 1) % kXSets], s + I + 1 + kXSets);
+                load_weights(w[(I + kWSets - 1) % kWSets], s + I + kWSets - 1);
+                __builtin_amdgcn_sched_barrier(0);
+                compute(halves, w[I % kWSets], I & 1, s + I);
+                if constexpr (I == 3) store_scales(sc, (s >> 2) + 1);
+            };
+            body(Int<0>()), body(Int<1>()), body(Int<2>()), body(Int<3>());
+        }
+    };
+    if (t.rows > 64) loop(Int<2>());
+    else loop(Int<1>());
+
+    // the sums are final here, with every lane active (the matrix instructions
+    // must not move into the guarded stores below)
+#pragma unroll
+    for (int j = 0; j < kMT; ++j)
+#pragma unroll
+        for (int i = 0; i < kNT; ++i) asm volatile("" : "+v"(acc[j][i]));
+
+    // lane (g, m): row 16 j + m, consecutive columns
+#pragma unroll
+    for (int j = 0; j < kMT; ++j) {
+        const int row = j * 16 + m;
+        const size_t yrow = (size_t)t.row0 + row;
+        if constexpr (EPI == kPlain) {
+            const int n = n0 + 16 * g;
+            if (row < t.rows && n < N) {
+                i32x4* to = reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.y) + yrow * N + n);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 a = acc[j][2 * h], b = acc[j][2 * h + 1];
+                    to[h] = i32x4{(int)pack_bf16x2(a[0], a[1]), (int)pack_bf16x2(a[2], a[3]),
                                   (int)pack_bf16x2(b[0], b[1]), (int)pack_bf16x2(b[2], b[3])};
-                } else {
-                    // the four lanes of a row hold a block of 32
-                    uint32_t x = 0u;
+                }
+            }
+        } else {
+            const int n = n0 + 8 * g;
+            f32x4 a, b;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) x = max(x, max(mag(a[c]), mag(b[c])));
-                    x = max(x, (uint32_t)__shfl_xor((int)x, 16, kWave));
-                    x = max(x, (uint32_t)__shfl_xor((int)x, 32, kWave));
-                    const uint32_t s = mx_scale(__uint_as_float(x));
-                    if (row < t.rows && n < N) {
-                        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + (yrow * N + n) / 2) =
-                            mx_codes4(a[0], a[1], a[2], a[3], s) | mx_codes4(b[0], b[1], b[2], b[3], s) << 16;
-                        if (g == 0) p.ys[yrow * (N / 32) + n / 32] = (uint8_t)s;
-                    }
+            for (int c = 0; c < 4; ++c) {
+                a[c] = gated(acc[j][0][c], acc[j][2][c]);
+                b[c] = gated(acc[j][1][c], acc[j][3][c]);
+            }
+            if constexpr (EPI == kGated) {
+                if (row < t.rows && n < N)
+                    *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.y) + yrow * N + n) =
+                        i32x4{(int)pack_bf16x2(a[0], a[1]), (int)pack_bf16x2(a[2], a[3]),
+                              (int)pack_bf16x2(b[0], b[1]), (int)pack_bf16x2(b[2], b[3])};
+            } else {
+                // the four lanes of a row hold a block of 32
+                uint32_t x = 0u;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x = max(x, max(mag(a[c]), mag(b[c])));
+                x = max(x, (uint32_t)__shfl_xor((int)x, 16, kWave));
+                x = max(x, (uint32_t)__shfl_xor((int)x, 32, kWave));
+                const uint32_t e = mx_scale(x);
+                if (row < t.rows && n < N) {
+                    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + (yrow * N + n) / 2) =
+                        mx_codes4(a[0], a[1], a[2], a[3], e) | mx_codes4(b[0], b[1], b[2], b[3], e) << 16;
+                    if (g == 0) p.ys[yrow * (N / 32) + n / 32] = (uint8_t)e;
                 }
             }
         }
@@ -628,7 +683,7 @@ template <bool FP8, int EPI>
 hipError_t launch_one(const Product& p, long pairs, hipStream_t stream) {
     if (pairs / p.rows.E < 32)
         return launch_tiles<16>(thin_kernel<FP8, EPI, 1, 4, 2>, p, pairs, kCols<EPI>, 256, stream);
-    return launch_tiles<kTileBM<FP8>>(tile_kernel<FP8, EPI>, p, pairs, kWavesN * kCols<EPI>, kThreads, stream);
+    return launch_tiles<kTileRows>(tile_kernel<FP8, EPI>, p, pairs, kTileWaves * kCols<EPI>, kTileThreads, stream);
 }
 
 template <bool FP8>

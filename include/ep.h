@@ -390,7 +390,8 @@ EP_API int ep_mxfp4_dequantize(int64_t rows, int32_t cols, const void* codes, co
  * the codes' values exactly; with EP_TYPE_FP8_E4M3 the sum over each 128
  * columns is multiplied by the row's fp32 scale and added up.
  *   x_type         EP_TYPE_FP8_E4M3 (ep_dispatch's payload) or EP_TYPE_MXFP4
- *   in_features    K, a multiple of 128, 128 <= K <= 32768
+ *   in_features    K, a multiple of 128 for FP8 and of 32 for MXFP4 rows,
+ *                  K <= 32768
  *   out_features   N, a multiple of 32, 32 <= N <= 32768
  *   x              device, [T*k, K] e4m3 codes or [T*k, K/2] bytes of MXFP4
  *                  codes, 16-byte aligned, in ep_get_layout's receive rows
@@ -399,7 +400,7 @@ EP_API int ep_mxfp4_dequantize(int64_t rows, int32_t cols, const void* codes, co
  *   expert_offset  device, int32 [E + 1] from ep_get_layout (entries are
  *                  clamped to [0, T*k]; it must not descend)
  *   w              device, MXFP4 codes [E, N, K/2], 16-byte aligned
- *   w_scales       device, bytes [E, N, K/32]
+ *   w_scales       device, bytes [E, N, K/32], 4-byte aligned
  *   y              device, bf16 [T*k, N] out, 16-byte aligned
  * cfg gives T, k and E; its hidden size takes no part.  The host does not wait
  * for the counts.  Deterministic. */

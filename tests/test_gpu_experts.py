@@ -114,6 +114,13 @@ def test_products(act, gate, counts, K, N, cap):
     Case(len(counts) * 1000 + K + N, counts, K, N, act, gate, cap, spare=0 if cap else 3).check("%s" % (counts[:8],))
 
 
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("counts", [FEW, MANY])
+@pytest.mark.parametrize("K,N", [(32, 32), (64, 64), (96, 32), (160, 288), (544, 64), (672, 96), (1440, 160)])
+def test_mxfp4_rows_of_any_blocks(counts, K, N, gate):
+    Case(K * 3 + N, counts, K, N, "mxfp4", gate, None, spare=1).check("%d columns" % K)
+
+
 @pytest.mark.parametrize("act", ["fp8", "mxfp4"])
 @pytest.mark.parametrize("counts,K,N,cap", [(FEW, 384, 96, None), (MANY, 640, 288, None), (FEW, 256, 64, 40),
                                             ([40] * 12, 512, 96, 64)])

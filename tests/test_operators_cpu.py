@@ -56,7 +56,8 @@ COMMON = [
     ({1: 0}, BAD), ({1: 192}, BAD), ({1: -128}, BAD), ({1: 32768 + 128}, UNSUP),
     ({2: 0}, BAD), ({2: 48}, BAD), ({2: -32}, BAD), ({2: 32768 + 32}, UNSUP),
     ({3: None}, BAD), ({4: None}, BAD), ({5: None}, BAD), ({6: None}, BAD), ({7: None}, BAD),
-    ({3: FAKE + 8}, ALIGN), ({4: FAKE + 2}, ALIGN), ({5: FAKE + 2}, ALIGN), ({6: FAKE + 8}, ALIGN),
+    ({3: FAKE + 8}, ALIGN), ({4: FAKE + 2}, ALIGN), ({5: FAKE + 2}, ALIGN), ({6: FAKE + 8}, ALIGN), ({7: FAKE + 2}, ALIGN),
+    ({0: MX, 1: 16}, BAD), ({0: MX, 1: 100}, BAD), ({0: MX, 1: 32768 + 32}, UNSUP),
 ]
 
 
