@@ -45,7 +45,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp8 = 0, kFp4 = 4;  // matrix instruction operand formats
 constexpr int kStep = 128;         // columns of a matrix instruction
-constexpr int kNT = 4;             // 16-row weight tiles per wavefront
+constexpr int kThinNT = 4, kTileNT = 8;  // 16-row weight tiles per wavefront
 constexpr int kUnit = 127;         // E8M0 scale of 1
 
 enum Epilogue { kPlain, kGated, kGatedMx };
@@ -57,9 +57,18 @@ struct Int {
     __device__ constexpr operator int() const { return I; }
 };
 
-// Output columns of a wavefront's kNT weight tiles.
-template <int EPI>
-constexpr int kCols = EPI == kPlain ? 16 * kNT : 8 * kNT;
+// f(Int<0>()) ... f(Int<N - 1>())
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(Int<N - 1>());
+    }
+}
+
+// Output columns of a wavefront's NT weight tiles.
+template <int EPI, int NT>
+constexpr int kCols = EPI == kPlain ? 16 * NT : 8 * NT;
 
 // One lane's 32 columns of an activation row (16-byte pieces).
 template <bool FP8>
@@ -68,13 +77,14 @@ struct XPiece {
 };
 
 // The E4M3 codes of magnitude 2 and above (bit 6 set), zero in the others'
-// places.
+// places: v_perm's selectors 8 .. 11 replicate the sign bits of bytes 1 and 3
+// of its second and of its first source.
 __device__ __forceinline__ i32x4 upper_codes(i32x4 v) {
     i32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t one = ((uint32_t)v[i] >> 6) & 0x01010101u;
-        r[i] = v[i] & (int)((one << 8) - one);
+        const uint32_t odd = (uint32_t)v[i] << 1, even = (uint32_t)v[i] << 9;
+        r[i] = v[i] & (int)__builtin_amdgcn_perm(odd, even, 0x0B090A08u);
     }
     return r;
 }
@@ -94,15 +104,35 @@ __device__ __forceinline__ f32x4 multiply(i32x4 w, int ws, const XPiece<FP8>& x,
                                                             XB, xs);
 }
 
-// Row of the weights that lane row `a` (0 .. 15) of tile 0 loads, for output
-// columns from n0 on, and how many rows further tile i's row lies.
-template <int EPI>
-__device__ __forceinline__ int weight_row(int n0, int a) {
-    return n0 + (EPI == kPlain ? kNT : kNT / 2) * 4 * (a >> 2) + (a & 3);
+// The same in place for MXFP4 operands, with the sums in accumulation
+// registers; both scales are byte B of their words.  Written out because the
+// compiler, asked for the full register file, moves sums between registers
+// around every instruction.  The wait states ahead cover an operand that an
+// ordinary instruction has just written; whoever reads the sums waits first.
+template <int B>
+__device__ __forceinline__ void multiply_in_place(f32x4& c, i32x4 w, int ws, i32x4 x, int xs) {
+    if constexpr (B == 0)
+        asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+            : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs));
+    else if constexpr (B == 1)
+        asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] "
+            "cbsz:4 blgp:4" : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs));
+    else if constexpr (B == 2)
+        asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+            : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs));
+    else
+        asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] "
+            "cbsz:4 blgp:4" : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs));
 }
-template <int EPI>
-__device__ __forceinline__ int tile_rows(int i, int N) {
-    return EPI == kPlain ? 4 * i : (i >= kNT / 2 ? N : 0) + 4 * (i % (kNT / 2));
+
+// Row of the weights that lane row `a` (0 .. 15) of tile i loads, for output
+// columns from n0 on; -1 past the last column (N is a multiple of 32, so that
+// is for all of a tile or none).
+template <int EPI, int NT>
+__device__ __forceinline__ int weight_row(int n0, int i, int a, int N) {
+    constexpr int kTiles = EPI == kPlain ? NT : NT / 2;
+    const int c = i % kTiles, n = n0 + 32 * (c >> 1) + 8 * (a >> 2) + 4 * (c & 1) + (a & 3);
+    return n < N ? n + (i >= kTiles ? N : 0) : -1;
 }
 
 // Byte offset that lies outside every buffer resource here (all are below
@@ -206,14 +236,18 @@ struct Product {
 };
 
 // Buffer resources of a tile's rows and of its expert's weights.
+// The rows' scales start xs_lead bytes into theirs, which is aligned to words.
 template <bool FP8, int EPI>
 struct Sources {
     __amdgpu_buffer_rsrc_t x, xs, w, ws;
+    int xs_lead;
     __device__ __forceinline__ Sources(const Product& p, const Tile& t) {
         const uint32_t xrow = FP8 ? p.K : p.K / 2, srow = FP8 ? p.K / 128 * 4 : p.K / 32;
         const uint32_t wrows = EPI == kPlain ? p.N : 2 * p.N;
         x = buffer_rsrc(p.x + (size_t)t.row0 * xrow, t.rows * xrow);
-        xs = buffer_rsrc(static_cast<const uint8_t*>(p.xs) + (size_t)t.row0 * srow, t.rows * srow);
+        const size_t first = (size_t)t.row0 * srow;
+        xs_lead = (int)(first & 3);
+        xs = buffer_rsrc(static_cast<const uint8_t*>(p.xs) + (first - xs_lead), (t.rows * srow + xs_lead + 3) & ~3u);
         w = buffer_rsrc(p.w + (size_t)t.e * wrows * (p.K / 2), wrows * (uint32_t)(p.K / 2));
         ws = buffer_rsrc(p.ws + (size_t)t.e * wrows * (p.K / 32), wrows * (uint32_t)(p.K / 32));
     }
@@ -244,7 +278,7 @@ __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0
 // next piece while the present one is multiplied.
 template <bool FP8, int EPI, int MT, int KS, int STEPS>
 __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
-    constexpr int BM = 16 * MT;
+    constexpr int BM = 16 * MT, kNT = kThinNT;
     __shared__ f32x4 part[KS][MT * kNT][kWave];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, m = lane & 15;
@@ -261,31 +295,31 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
     if (!find_tile<BM>(p.rows, ntiles, blockIdx.x, t)) return;
     {
         const Sources<FP8, EPI> src(p, t);
-        const int n0 = t.n * kCols<EPI>;
-        // a lane's weight rows are all inside or all outside (N is a multiple
-        // of 32); scalar offsets take no part in the bounds check
-        const int wrow = weight_row<EPI>(n0, m);
-        const int wat = wrow < N ? wrow * (K / 2) + g * 16 : kOutside;
-        const int wsat = wrow < N ? wrow * (K / 32) + g : kOutside;
-        int xat[MT], xsat[MT];
+        const int n0 = t.n * kCols<EPI, kNT>;
+        int wat[kNT], wsat[kNT], xat[MT], xsat[MT];
+#pragma unroll
+        for (int i = 0; i < kNT; ++i) {
+            const int row = weight_row<EPI, kNT>(n0, i, m, N);
+            wat[i] = row >= 0 ? row * (K / 2) + g * 16 : kOutside;
+            wsat[i] = row >= 0 ? row * blocks + g : kOutside;
+        }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             const int row = j * 16 + m;
             xat[j] = row * (FP8 ? K : K / 2) + g * 16;
-            xsat[j] = FP8 ? row * (K / 32) : row * (K / 32) + g;
+            xsat[j] = row < t.rows ? src.xs_lead + row * blocks + (FP8 ? 0 : g) : kOutside;
         }
         // past the last step (and the last block of MXFP4 rows) these read zeros
         const auto load = [&](Piece& q, int step0) {
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int step = step0 + s, b = step * 4 + g;
-                const int wto = offset_if(wat, b, blocks), wsto = offset_if(wsat, b, blocks);
 #pragma unroll
                 for (int i = 0; i < kNT; ++i) {
-                    const int row = tile_rows<EPI>(i, N);
-                    q.w[s][i] = __builtin_amdgcn_raw_buffer_load_b128(src.w, wto, row * (K / 2) + step * 64, kCached);
-                    q.ws[s][i] =
-                        (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.ws, wsto, row * blocks + step * 4, kCached);
+                    q.w[s][i] = __builtin_amdgcn_raw_buffer_load_b128(src.w, offset_if(wat[i], b, blocks), step * 64,
+                                                                       kCached);
+                    q.ws[s][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                        src.ws, offset_if(wsat[i], b, blocks), step * 4, kCached);
                 }
 #pragma unroll
                 for (int j = 0; j < MT; ++j) {
@@ -363,11 +397,11 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
             return s;
         };
         // four columns of a row to a thread, the threads of a row side by side
-        constexpr int kPer = kCols<EPI> / 4;
+        constexpr int kPer = kCols<EPI, kNT> / 4;
         for (int q = threadIdx.x; q < BM * kPer; q += 64 * KS) {
-            const int row = q / kPer, c = q % kPer;      // c = (kNT or kNT / 2) g + i
-            constexpr int kI = EPI == kPlain ? kNT : kNT / 2;
-            const int from = (c / kI) * 16 + (row & 15), tile = (row >> 4) * kNT + c % kI;
+            const int row = q / kPer, c = q % kPer;      // c = 8 h + 2 g + i % 2
+            constexpr int kI = kNT / 2;
+            const int from = (c >> 1 & 3) * 16 + (row & 15), tile = (row >> 4) * kNT + 2 * (c >> 3) + (c & 1);
             f32x4 o = sum(tile, from);
             const int n = n0 + 4 * c;
             const size_t yrow = (size_t)t.row0 + row;
@@ -403,262 +437,285 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
 
 // ------------------------------------------------- many rows per expert
 
-// A workgroup takes 128 rows by 8 x kCols columns with 8 wavefronts side by
-// side, each all 128 rows by kCols columns.  The rows of a 128-column step go
-// through LDS (two buffers), as do the weights' scales of four steps at a
-// time, turned so that a lane reads its four tiles' bytes at once; a
-// wavefront's weights are its own and go straight to registers, several steps
-// ahead.  Every step has one barrier.  Tiles of up to 64 rows multiply only half.
-constexpr int kTileWaves = 8, kTileMT = 8, kTileRows = 16 * kTileMT, kTileThreads = 64 * kTileWaves;
+// A workgroup of 2 x 2 wavefronts takes 32 MT rows by 2 kCols columns, each
+// wavefront 16 MT rows by kCols columns.  Rows and weights of a 128-column step
+// go through LDS (two buffers): four lanes load 64 consecutive bytes of a row,
+// where an operand straight from memory would have four lanes read 16 bytes of
+// four rows and use the cache four times over.  The scales of four steps at a
+// time go through LDS with their 4 x 4 bytes turned, so that a lane gets the
+// four steps of its block in one word.  Every step has one barrier.
+// Two workgroups share a compute unit, and one multiplies while the other
+// waits.
+constexpr int kTileThreads = 256;
 
 template <bool FP8, int EPI>
-__global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p, int ntiles) {
-    constexpr int kMT = kTileMT;
-    constexpr int kChunks = FP8 ? 8 : 4;                         // 16-byte chunks of a row's step
-    constexpr int kPer = kTileRows * kChunks / kTileThreads;     // chunks staged by a thread
-    constexpr int kParts = FP8 ? 2 : 1;                          // FP8: low codes, then high codes
-    constexpr int kWSets = 2, kXSets = FP8 ? 1 : 2;    // steps of weights and rows in registers
-    __shared__ i32x4 rows_lds[2][kParts][kTileRows * kChunks];
-    __shared__ __align__(16) uint8_t xs_lds[2][kTileRows * 4];
-    __shared__ __align__(16) uint8_t ws_lds[2][4][kTileThreads * 4];
+__global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int ntiles) {
+    constexpr int MT = 4, NT = kTileNT, BM = 32 * MT, BW = 32 * NT;  // rows, weight rows
+    constexpr int kChunks = FP8 ? 8 : 4;                     // 16-byte chunks of a row's step
+    constexpr int kXPer = BM * kChunks / kTileThreads;       // chunks staged by a thread
+    constexpr int kWPer = BW * 4 / kTileThreads;
+    static_assert(BW == kTileThreads && BM <= kTileThreads);
+    __shared__ i32x4 rows_lds[2][BM * kChunks];
+    __shared__ i32x4 w_lds[2][BW * 4];
+    __shared__ i32x4 xs_lds[2][BM];
+    __shared__ i32x4 ws_lds[2][BW];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g = lane >> 4, m = lane & 15;
+    const int g = lane >> 4, m = lane & 15, wm = wave >> 1, wn = wave & 1;
     const int K = p.K, N = p.N, steps = (K + kStep - 1) / kStep, blocks = K / 32;
 
     // 16-byte chunk c of row r lies at a place of its own in the row, so that
-    // the eight rows read together fall into different banks
-    const auto place = [](int r, int c) {
-        if constexpr (FP8) return r * kChunks + (c ^ (r & 7));
-        else return r * kChunks + (c ^ ((r >> 1) & 3));
-    };
+    // the rows read together fall into different banks (measured: 223 bytes a
+    // clock and compute unit, of 256; without it, 123)
+    const auto place8 = [](int r, int c) { return r * 8 + (c ^ (r & 7)); };
+    const auto place4 = [](int r, int c) { return r * 4 + (c ^ (r >> 1 & 3)); };
+    const auto place = [&](int r, int c) { return FP8 ? place8(r, c) : place4(r, c); };
 
     Tile t;
-    if (!find_tile<kTileRows>(p.rows, ntiles, blockIdx.x, t)) return;
+    if (!find_tile<BM>(p.rows, ntiles, blockIdx.x, t)) return;
     const Sources<FP8, EPI> src(p, t);
-    const int n0 = (t.n * kTileWaves + wave) * kCols<EPI>;
+    const int n0 = t.n * 2 * kCols<EPI, NT>;  // of the workgroup
 
-    // this lane's weights
-    const int wrow = weight_row<EPI>(n0, m);
-    const int wat = wrow < N ? wrow * (K / 2) + g * 16 : kOutside;
-    // this thread's chunks of the rows: chunk tid and those kStride rows apart
-    constexpr int kStride = kTileThreads / kChunks;
-    const int xrow = tid / kChunks, xbytes = FP8 ? K : K / 2;
-    const int xat = xrow * xbytes + tid % kChunks * 16;
-    const int xto = place(xrow, tid % kChunks);
-    // its row scale: FP8 one of a row (four threads the same), MXFP4 one byte;
-    // row 16 i + c lies at 8 c + i, where the lanes c read their eight rows
-    const int srow = tid >> 2, sto = (srow & 15) * 8 + (srow >> 4);
-    // its weight row's scales: tile i, lane row a of this wavefront's tiles
-    const int vtile = lane >> 4, vrow = weight_row<EPI>(n0, m) + tile_rows<EPI>(vtile, N);
-    const int vat = wrow < N ? vrow * blocks : kOutside;
-    const int vshift = vat & 3;  // rows of scales need not be a multiple of 4 bytes
-
-    struct Staged {
-        i32x4 x[kPer];
-        int xs;
+    // this thread's chunks of the rows: chunk tid and those kXStride rows apart
+    constexpr int kXStride = kTileThreads / kChunks;
+    const int xbytes = FP8 ? K : K / 2, xrow = tid / kChunks, xto = place(xrow, tid % kChunks);
+    int xat[kXPer];
+#pragma unroll
+    for (int j = 0; j < kXPer; ++j) xat[j] = (xrow + j * kXStride) * xbytes + tid % kChunks * 16;
+    // its chunks of the weights: row 128 v + 16 i + a of LDS is wavefront column
+    // v's tile i, lane row a
+    const auto weight_at = [&](int r) {
+        return weight_row<EPI, NT>(n0 + (r >> 7) * kCols<EPI, NT>, r >> 4 & 7, r & 15, N);
     };
+    int wat[kWPer];
+#pragma unroll
+    for (int j = 0; j < kWPer; ++j) {
+        const int row = weight_at(tid / 4 + j * (kTileThreads / 4));
+        wat[j] = row >= 0 ? row * (K / 2) + (tid & 3) * 16 : kOutside;
+    }
+    const int wto = place4(tid / 4, tid & 3);  // and kTileThreads / 4 rows apart
+    // its row's and its weight row's scales; rows of scales need not be a
+    // multiple of 4 bytes
+    const int sat = tid % BM * blocks + src.xs_lead, vrow = weight_at(tid);
+    const int vat = vrow >= 0 ? vrow * blocks : kOutside;
+
     struct Scales {
         i32x4 v;
         int more;
     };
-    const auto load_rows = [&](Staged& q, int step) {
-        const int i = FP8 ? step : step * 4 + (tid & 3), n = FP8 ? steps : blocks;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int at = offset_if(xat + j * kStride * xbytes, i, n);
-            q.x[j] = __builtin_amdgcn_raw_buffer_load_b128(src.x, at, step * (FP8 ? 128 : 64), kCached);
-        }
-        if constexpr (FP8) {
-            q.xs = __builtin_amdgcn_raw_buffer_load_b32(src.xs, offset_if(srow * blocks, i, n), step * 4, kCached);
-        } else {
-            const int at = offset_if(srow * blocks + (tid & 3), i, n);
-            q.xs = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.xs, at, step * 4, kCached);
-        }
+    // the thread's chunks of a step, rows first, then weights
+    i32x4 st[kXPer + kWPer];
+    const auto load_chunk = [&](auto chunk, int step) {
+        constexpr int C = decltype(chunk)::value;
+        if constexpr (C < kXPer)
+            st[C] = __builtin_amdgcn_raw_buffer_load_b128(
+                src.x, offset_if(xat[C], step * 4 + (FP8 ? 0 : tid & 3), blocks), step * (FP8 ? 128 : 64), kCached);
+        else
+            st[C] = __builtin_amdgcn_raw_buffer_load_b128(
+                src.w, offset_if(wat[C - kXPer], step * 4 + (tid & 3), blocks), step * 64, kCached);
     };
-    const auto store_rows = [&](const Staged& q, int buf) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int to = xto + j * kStride * kChunks;
-            if constexpr (FP8) {
-                const i32x4 high = upper_codes(q.x[j]);
-                rows_lds[buf][0][to] = q.x[j] ^ high;
-                rows_lds[buf][kParts - 1][to] = high;
-            } else {
-                rows_lds[buf][0][to] = q.x[j];
-            }
-        }
-        if constexpr (FP8) *reinterpret_cast<int*>(&xs_lds[buf][sto * 4]) = q.xs;
-        else xs_lds[buf][(tid & 3) * kTileRows + sto] = (uint8_t)q.xs;
+    const auto store_chunk = [&](auto chunk, int buf) {
+        constexpr int C = decltype(chunk)::value;
+        if constexpr (C < kXPer) rows_lds[buf][xto + C * kXStride * kChunks] = st[C];
+        else w_lds[buf][wto + (C - kXPer) * kTileThreads] = st[C];
     };
-    const auto load_weights = [&](i32x4 (&w)[kNT], int step) {
-        const int at = offset_if(wat, step * 4 + g, blocks);
-#pragma unroll
-        for (int i = 0; i < kNT; ++i)
-            w[i] = __builtin_amdgcn_raw_buffer_load_b128(src.w, at, tile_rows<EPI>(i, N) * (K / 2) + step * 64,
-                                                         kCached);
+    const auto load_rows = [&](int step) { each<kXPer>([&](auto c) { load_chunk(c, step); }); };
+    const auto store_rows = [&](int buf) { each<kXPer>([&](auto c) { store_chunk(c, buf); }); };
+    const auto load_weights = [&](int step) {
+        each<kWPer>([&](auto c) { load_chunk(Int<kXPer + decltype(c)::value>(), step); });
+    };
+    const auto store_weights = [&](int buf) {
+        each<kWPer>([&](auto c) { store_chunk(Int<kXPer + decltype(c)::value>(), buf); });
     };
     // the scales of steps 4 four .. 4 four + 3: 16 bytes of a row, from the
     // aligned words that hold them
-    const auto load_scales = [&](Scales& q, int four) {
-        const int at = offset_if(vat - vshift, four * 16, blocks);
-        q.v = __builtin_amdgcn_raw_buffer_load_b128(src.ws, at, four * 16, kCached);
-        q.more = __builtin_amdgcn_raw_buffer_load_b32(src.ws, offset_if(at + 16, 0, vshift), four * 16, kCached);
+    const auto load_scales = [&](Scales& q, __amdgpu_buffer_rsrc_t r, int row_at, int four) {
+        const int at = offset_if(row_at & ~3, four * 16, blocks);
+        q.v = __builtin_amdgcn_raw_buffer_load_b128(r, at, four * 16, kCached);
+        q.more = __builtin_amdgcn_raw_buffer_load_b32(r, offset_if(at + 16, 0, row_at & 3), four * 16, kCached);
     };
-    const auto store_scales = [&](const Scales& q, int four) {
+    // ... zero past the row's end (those bytes are another row's), and with the
+    // steps as bytes of the blocks' words (turn) or as they are
+    const auto store_scales = [&](const Scales& q, i32x4& to, int row_at, int four, bool turn) {
+        uint32_t d[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const uint32_t lo = (uint32_t)q.v[s], hi = (uint32_t)(s < 3 ? q.v[s < 3 ? s + 1 : 3] : q.more);
-            const uint32_t d = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)vshift);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const bool in = four * 16 + s * 4 + b < blocks;  // bytes past the row are another row's
-                ws_lds[four & 1][s][wave * 256 + (b * 16 + m) * 4 + vtile] = in ? (uint8_t)(d >> (8 * b)) : 0;
-            }
+            const int n = min(max(blocks - four * 16 - s * 4, 0), 4);  // blocks of the step
+            d[s] = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)row_at & 3u) & (uint32_t)((1ull << (8 * n)) - 1);
+        }
+        if (turn) {
+            const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400), b = __builtin_amdgcn_perm(d[1], d[0], 0x07030602);
+            const uint32_t c = __builtin_amdgcn_perm(d[3], d[2], 0x05010400), e = __builtin_amdgcn_perm(d[3], d[2], 0x07030602);
+            to = i32x4{(int)__builtin_amdgcn_perm(c, a, 0x05040100), (int)__builtin_amdgcn_perm(c, a, 0x07060302),
+                       (int)__builtin_amdgcn_perm(e, b, 0x05040100), (int)__builtin_amdgcn_perm(e, b, 0x07060302)};
+        } else {
+            to = i32x4{(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
         }
     };
-
-    f32x4 acc[kMT][kNT];
-#pragma unroll
-    for (int j = 0; j < kMT; ++j)
-#pragma unroll
-        for (int i = 0; i < kNT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    constexpr int kHold = FP8 ? 1 : 4;  // row tiles read from LDS at a time
-    const int rx0 = place(m, g), rx1 = place(m, FP8 ? g + 4 : g);
-    const auto compute = [&](auto halves, const i32x4 (&w)[kNT], int buf, int step) {
-        const int ws = *reinterpret_cast<const int*>(&ws_lds[(step >> 2) & 1][step & 3][wave * 256 + lane * 4]);
-        // row tiles H .. H + kHold - 1
-        const auto rows = [&](auto first) {
-            constexpr int H = decltype(first)::value;
-            XPiece<FP8> x[kHold], high[kHold];
-#pragma unroll
-            for (int j = 0; j < kHold; ++j) {
-                x[j].v[0] = rows_lds[buf][0][rx0 + (H + j) * 16 * kChunks];
-                if constexpr (FP8) {
-                    x[j].v[1] = rows_lds[buf][0][rx1 + (H + j) * 16 * kChunks];
-                    high[j].v[0] = rows_lds[buf][kParts - 1][rx0 + (H + j) * 16 * kChunks];
-                    high[j].v[1] = rows_lds[buf][kParts - 1][rx1 + (H + j) * 16 * kChunks];
-                }
-            }
-            if constexpr (FP8) {
-                const float sc = *reinterpret_cast<const float*>(&xs_lds[buf][(m * kMT + H) * 4]);
-                f32x4 r[kNT];
-                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                r[0] = multiply<true, 0, 0>(w[0], ws, x[0], kUnit, zero);
-                r[1] = multiply<true, 1, 0>(w[1], ws, x[0], kUnit, zero);
-                r[2] = multiply<true, 2, 0>(w[2], ws, x[0], kUnit, zero);
-                r[3] = multiply<true, 3, 0>(w[3], ws, x[0], kUnit, zero);
-                r[0] = multiply<true, 0, 0>(w[0], ws, high[0], kUnit, r[0]);
-                r[1] = multiply<true, 1, 0>(w[1], ws, high[0], kUnit, r[1]);
-                r[2] = multiply<true, 2, 0>(w[2], ws, high[0], kUnit, r[2]);
-                r[3] = multiply<true, 3, 0>(w[3], ws, high[0], kUnit, r[3]);
-#pragma unroll
-                for (int i = 0; i < kNT; ++i) {
-                    const f32x4 o = acc[H][i];
-                    acc[H][i] = f32x4{__builtin_fmaf(sc, r[i][0], o[0]), __builtin_fmaf(sc, r[i][1], o[1]),
-                                      __builtin_fmaf(sc, r[i][2], o[2]), __builtin_fmaf(sc, r[i][3], o[3])};
-                }
-            } else {
-                const int sc = *reinterpret_cast<const int*>(&xs_lds[buf][g * kTileRows + m * kMT + H]);
-                const auto column = [&](auto i) {
-                    constexpr int I = decltype(i)::value;
-                    acc[H + 0][I] = multiply<false, I, 0>(w[I], ws, x[0], sc, acc[H + 0][I]);
-                    acc[H + 1][I] = multiply<false, I, 1>(w[I], ws, x[1 % kHold], sc, acc[H + 1][I]);
-                    acc[H + 2][I] = multiply<false, I, 2>(w[I], ws, x[2 % kHold], sc, acc[H + 2][I]);
-                    acc[H + 3][I] = multiply<false, I, 3>(w[I], ws, x[3 % kHold], sc, acc[H + 3][I]);
-                };
-                column(Int<0>()), column(Int<1>()), column(Int<2>()), column(Int<3>());
-            }
-        };
-        const auto half = [&](auto first) {
-            constexpr int H = decltype(first)::value;
-            rows(Int<H>());
-            if constexpr (kHold == 1) rows(Int<H + 1>()), rows(Int<H + 2>()), rows(Int<H + 3>());
-        };
-        half(Int<0>());
-        if constexpr (halves > 1) half(Int<4>());
-    };
-
-    Staged st[kXSets];
-    i32x4 w[kWSets][kNT];
     Scales sc;
-    load_scales(sc, 0);
-    load_rows(st[0], 0);
+    const auto load_row_scales = [&](int four) { load_scales(sc, src.xs, sat, four); };
+    const auto load_weight_scales = [&](int four) { load_scales(sc, src.ws, vat, four); };
+    const auto store_row_scales = [&](int four) { store_scales(sc, xs_lds[four & 1][tid % BM], sat, four, !FP8); };
+    const auto store_weight_scales = [&](int four) { store_scales(sc, ws_lds[four & 1][tid], vat, four, true); };
+
+    f32x4 acc[MT][NT];
 #pragma unroll
-    for (int i = 0; i + 1 < kWSets; ++i) load_weights(w[i], i);
-    store_scales(sc, 0);
-    store_rows(st[0], 0);
+    for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int i = 1; i <= kXSets; ++i) load_rows(st[i % kXSets], i);
-    // Step s: its rows and scales are in LDS when every wavefront is past the
-    // barrier, and the other buffers are no longer read.  Four steps at a time,
-    // without conditions: loads past the last step read zeros, which add
-    // nothing, and each wait counts exactly what is in flight.
-    const auto loop = [&](auto halves) {
-        for (int s = 0; s < steps; s += 4) {
-            const auto body = [&](auto phase) {
-                constexpr int I = decltype(phase)::value;
-                __syncthreads();
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (I == 0) load_scales(sc, (s >> 2) + 1);
-                store_rows(st[(I + 1) % kXSets], (I + 1) & 1);
-                load_rows(st[(I + 1) % kXSets], s + I + 1 + kXSets);
-                load_weights(w[(I + kWSets - 1) % kWSets], s + I + kWSets - 1);
-                __builtin_amdgcn_sched_barrier(0);
-                compute(halves, w[I % kWSets], I & 1, s + I);
-                if constexpr (I == 3) store_scales(sc, (s >> 2) + 1);
-            };
-            body(Int<0>()), body(Int<1>()), body(Int<2>()), body(Int<3>());
+        for (int i = 0; i < NT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // this wavefront's operands: of a step, and the scales of four
+    struct Operands {
+        i32x4 w[NT], x[FP8 ? 1 : MT];
+    };
+    struct OperandScales {
+        int w[NT], x[FP8 ? 1 : MT];
+    };
+    constexpr int kHalf = 16 * MT;
+    const int rx0 = place(wm * kHalf + m, g), rx1 = place(wm * kHalf + m, FP8 ? g + 4 : g);
+    const int rw = place4(wn * 128 + m, g);
+    const auto read_scales = [&](OperandScales& o, int four) {
+        const int* from = reinterpret_cast<const int*>(&ws_lds[four & 1][wn * 128 + m]) + g;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o.w[i] = from[i * 64];
+        if constexpr (!FP8) {
+            const int* rows = reinterpret_cast<const int*>(&xs_lds[four & 1][wm * kHalf + m]) + g;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) o.x[j] = rows[j * 64];
         }
     };
-    if (t.rows > 64) loop(Int<2>());
-    else loop(Int<1>());
+    const auto read_weights = [&](Operands& o, int buf) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o.w[i] = w_lds[buf][rw + i * 64];
+    };
+    // row tile J of step 4 four + I
+    const auto multiply_rows = [&](auto tile, auto phase, const Operands& o, const OperandScales& sc, int buf,
+                                   int four) {
+        constexpr int J = decltype(tile)::value, I = decltype(phase)::value;
+        if constexpr (!FP8) {
+            each<NT>([&](auto i) {
+                constexpr int T = decltype(i)::value;
+                XPiece<false> q;
+                q.v[0] = o.x[J];
+                acc[J][T] = multiply<false, I, I>(o.w[T], sc.w[T], q, sc.x[J], acc[J][T]);
+            });
+        } else {
+            XPiece<true> low, high;
+            low.v[0] = rows_lds[buf][rx0 + J * 128], low.v[1] = rows_lds[buf][rx1 + J * 128];
+            const float xs = __int_as_float(reinterpret_cast<const int*>(&xs_lds[four & 1][wm * kHalf + J * 16 + m])[I]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) high.v[h] = upper_codes(low.v[h]), low.v[h] ^= high.v[h];
+            each<NT / 4>([&](auto quarter) {
+                constexpr int Q = decltype(quarter)::value * 4;
+                f32x4 r[4];
+                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = multiply<true, I, 0>(o.w[Q + i], sc.w[Q + i], low, kUnit, zero);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = multiply<true, I, 0>(o.w[Q + i], sc.w[Q + i], high, kUnit, r[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[J][Q + i][c] = __builtin_fmaf(xs, r[i][c], acc[J][Q + i][c]);
+            });
+        }
+    };
+
+    // Step s: its operands are in LDS when every wavefront is past the barrier,
+    // and the other buffer is no longer read.  Four steps at a time, without conditions: loads past the last step read zeros,
+    // which add nothing, and each wait counts exactly what is in flight.  The
+    // scheduling barriers keep the compiler to the order of the parts.
+    load_row_scales(0);
+    load_rows(0);
+    load_weights(0);
+    store_row_scales(0);
+    load_weight_scales(0);
+    store_rows(0);
+    store_weights(0);
+    load_weights(1);
+    if constexpr (!FP8) load_rows(1);
+    store_weight_scales(0);
+    load_row_scales(1);
+    Operands o;
+    OperandScales os;
+    for (int four = 0; four * 4 < steps; ++four) {
+        each<4>([&](auto phase) {
+            constexpr int I = decltype(phase)::value, B = I & 1;
+            const int s = four * 4 + I;
+            __syncthreads();
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (I == 0) read_scales(os, four);
+            read_weights(o, B);
+            if constexpr (FP8) {
+                // weights and rows take turns in the registers, half a step each
+                store_weights(1 - B);
+                load_rows(s + 1);
+                multiply_rows(Int<0>(), phase, o, os, B, four);
+                multiply_rows(Int<1>(), phase, o, os, B, four);
+                __builtin_amdgcn_sched_barrier(0);
+                store_rows(1 - B);
+                load_weights(s + 2);
+                multiply_rows(Int<2>(), phase, o, os, B, four);
+                multiply_rows(Int<3>(), phase, o, os, B, four);
+            } else {
+#pragma unroll
+                for (int j = 0; j < MT; ++j) o.x[j % (FP8 ? 1 : MT)] = rows_lds[B][rx0 + j * 64];
+                multiply_rows(Int<0>(), phase, o, os, B, four);
+                __builtin_amdgcn_sched_barrier(0);
+                store_rows(1 - B);
+                store_weights(1 - B);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply_rows(Int<1>(), phase, o, os, B, four);
+                __builtin_amdgcn_sched_barrier(0);
+                load_rows(s + 2);
+                load_weights(s + 2);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply_rows(Int<2>(), phase, o, os, B, four);
+                multiply_rows(Int<3>(), phase, o, os, B, four);
+            }
+            if constexpr (I == 0) store_row_scales(four + 1), load_weight_scales(four + 1);
+            if constexpr (I == 2) store_weight_scales(four + 1), load_row_scales(four + 2);
+        });
+    }
 
     // the sums are final here, with every lane active (the matrix instructions
     // must not move into the guarded stores below)
 #pragma unroll
-    for (int j = 0; j < kMT; ++j)
+    for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int i = 0; i < kNT; ++i) asm volatile("" : "+v"(acc[j][i]));
+        for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(acc[j][i]));
 
-    // lane (g, m): row 16 j + m, consecutive columns
+    // lane (g, m): row 16 j + m, eight columns of each 32
 #pragma unroll
-    for (int j = 0; j < kMT; ++j) {
-        const int row = j * 16 + m;
+    for (int j = 0; j < MT; ++j) {
+        const int row = wm * kHalf + j * 16 + m;
         const size_t yrow = (size_t)t.row0 + row;
-        if constexpr (EPI == kPlain) {
-            const int n = n0 + 16 * g;
-            if (row < t.rows && n < N) {
-                i32x4* to = reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.y) + yrow * N + n);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const f32x4 a = acc[j][2 * h], b = acc[j][2 * h + 1];
-                    to[h] = i32x4{(int)pack_bf16x2(a[0], a[1]), (int)pack_bf16x2(a[2], a[3]),
-                                  (int)pack_bf16x2(b[0], b[1]), (int)pack_bf16x2(b[2], b[3])};
+        for (int h = 0; h < kCols<EPI, NT> / 32; ++h) {
+            const int n = n0 + wn * kCols<EPI, NT> + 32 * h + 8 * g;
+            const bool on = row < t.rows && n < N;
+            f32x4 a = acc[j][2 * h], b = acc[j][2 * h + 1];
+            if constexpr (EPI != kPlain) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    a[c] = gated(a[c], acc[j][2 * h + NT / 2][c]);
+                    b[c] = gated(b[c], acc[j][2 * h + 1 + NT / 2][c]);
                 }
             }
-        } else {
-            const int n = n0 + 8 * g;
-            f32x4 a, b;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                a[c] = gated(acc[j][0][c], acc[j][2][c]);
-                b[c] = gated(acc[j][1][c], acc[j][3][c]);
-            }
-            if constexpr (EPI == kGated) {
-                if (row < t.rows && n < N)
+            if constexpr (EPI != kGatedMx) {
+                if (on)
                     *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.y) + yrow * N + n) =
                         i32x4{(int)pack_bf16x2(a[0], a[1]), (int)pack_bf16x2(a[2], a[3]),
                               (int)pack_bf16x2(b[0], b[1]), (int)pack_bf16x2(b[2], b[3])};
             } else {
                 // the four lanes of a row hold a block of 32
-                uint32_t x = 0u;
+                uint32_t v = 0u;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) x = max(x, max(mag(a[c]), mag(b[c])));
-                x = max(x, (uint32_t)__shfl_xor((int)x, 16, kWave));
-                x = max(x, (uint32_t)__shfl_xor((int)x, 32, kWave));
-                const uint32_t e = mx_scale(x);
-                if (row < t.rows && n < N) {
+                for (int c = 0; c < 4; ++c) v = max(v, max(mag(a[c]), mag(b[c])));
+                v = max(v, (uint32_t)__shfl_xor((int)v, 16, kWave));
+                v = max(v, (uint32_t)__shfl_xor((int)v, 32, kWave));
+                const uint32_t e = mx_scale(v);
+                if (on) {
                     *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + (yrow * N + n) / 2) =
                         mx_codes4(a[0], a[1], a[2], a[3], e) | mx_codes4(b[0], b[1], b[2], b[3], e) << 16;
                     if (g == 0) p.ys[yrow * (N / 32) + n / 32] = (uint8_t)e;
@@ -668,12 +725,314 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p, int nt
     }
 }
 
+// ------------------------------------- many rows per expert, MXFP4 rows
+
+// A workgroup of 2 x 2 wavefronts takes 256 rows by 2 kCols columns, each
+// wavefront 128 rows by kCols columns: half of what LDS and the cache move for
+// a product in tile_kernel.  A wavefront has a SIMD to itself, its sums fill
+// the accumulation registers, and it reads the next step's operands between the
+// matrix instructions of the present one.  Rows and weights go from memory
+// straight to LDS, four buffers deep, three steps ahead; s_waitcnt counts them
+// (loads complete in order).  There is one workgroup per compute unit, which
+// goes from tile to tile and starts the next tile's loads before it stores the
+// last one's results.  K is a multiple of 128.
+constexpr int kWideRows = 256, kWideGrid = 256;  // one workgroup for each of 256 compute units
+
+// Tiles before each expert, its first row and its rows, in LDS.
+struct TileTable {
+    int32_t upto[1024], first[1024], rows[1024];
+    int32_t part[4];
+
+    __device__ __forceinline__ void fill(const Rows& list) {
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+        int n[4], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = tid * 4 + i;
+            rows[e] = list.count(e);
+            first[e] = list.first(e);
+            n[i] = (rows[e] + kWideRows - 1) / kWideRows;
+            mine += n[i];
+        }
+        const int sum = wave_inclusive_sum(mine);
+        if (lane == 63) part[wave] = sum;
+        __syncthreads();
+        int before = sum - mine;
+        for (int w = 0; w < wave; ++w) before += part[w];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            before += n[i];
+            upto[tid * 4 + i] = before;
+        }
+        __syncthreads();
+    }
+
+    // find_tile's order
+    __device__ __forceinline__ bool find(uint32_t ntiles, uint32_t v, Tile& t) const {
+        constexpr uint32_t kGroup = 4;
+        const int lane = threadIdx.x & 63;
+        const uint32_t n = (uint32_t)__builtin_amdgcn_readfirstlane(upto[1023]) * ntiles;
+        if (v >= n) return false;
+        const uint32_t q = n >> 3, r = n & 7, x = v & 7;
+        const uint32_t at = x * q + (x < r ? x : r) + (v >> 3);
+        const int row_tile = (int)(at / ntiles);
+        const int run = __builtin_ctzll(__ballot(upto[lane * 16 + 15] > row_tile));
+        const int e = run * 16 + __builtin_ctzll(__ballot(upto[run * 16 + (lane & 15)] > row_tile));
+        const int start = e > 0 ? __builtin_amdgcn_readfirstlane(upto[e > 0 ? e - 1 : 0]) : 0;
+        const uint32_t have = (uint32_t)(__builtin_amdgcn_readfirstlane(upto[e]) - start);
+        const uint32_t local = at - (uint32_t)start * ntiles;
+        const uint32_t group = local / (kGroup * ntiles), in = local - group * kGroup * ntiles;
+        const uint32_t wide = min(kGroup, have - group * kGroup);
+        const int m = (int)(group * kGroup + in % wide) * kWideRows;
+        t.e = e;
+        t.n = (int)(in / wide);
+        t.row0 = __builtin_amdgcn_readfirstlane(first[e]) + m;
+        t.rows = min(kWideRows, __builtin_amdgcn_readfirstlane(rows[e]) - m);
+        return true;
+    }
+};
+
+// A buffer resource in four scalar registers, and a load from it to LDS, 16
+// bytes a lane, in the order of the lanes from byte `to` of LDS on.  Written
+// out because the compiler has every later read of LDS wait for all of them;
+// wait_loads says when they are needed.  (They write no registers.)
+__device__ __forceinline__ i32x4 resource_words(const void* base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)(a >> 32)),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t to, int at, int from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(to), "v"(at), "s"(r), "s"(from) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <int EPI>
+__global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int ntiles) {
+    constexpr int MT = 8, NT = kTileNT, BM = kWideRows, BW = 32 * NT;
+    static_assert(BM == kTileThreads && BW == kTileThreads);
+    __shared__ i32x4 rows_lds[2][BM * 8];  // two steps of a row side by side
+    __shared__ i32x4 w_lds[2][BW * 8];
+    __shared__ i32x4 xs_lds[BM * 2];       // eight steps' scales of a row
+    __shared__ i32x4 ws_lds[BW * 2];
+    __shared__ TileTable table;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, m = lane & 15, wm = wave >> 1, wn = wave & 1;
+    const int K = p.K, N = p.N, steps = K / kStep, blocks = K / 32, row_bytes = K / 2;
+
+    table.fill(p.rows);
+    Tile t;
+    uint32_t v = blockIdx.x;
+    if (!table.find(ntiles, v, t)) return;
+
+    // LDS is written in order of the threads, eight to the 128 bytes of a row
+    // (a whole line of the cache); which 16 bytes a thread brings puts the rows
+    // that are read together into different banks.  Load j (0 .. 7) brings rows
+    // tid / 8 + 32 j; for the weights that is wavefront column j / 4's tiles
+    // 2 (j % 4) and 2 (j % 4) + 1, 32 columns in a row.
+    const int row8 = tid >> 3, chunk = (tid & 7) ^ (row8 & 7);
+    const int xat = row8 * row_bytes + chunk * 16;
+    const int wat = (8 * (row8 >> 2 & 3) + 4 * (row8 >> 4) + (row8 & 3)) * row_bytes + chunk * 16;
+    i32x4 rows_src, xs_src, w_src, ws_src;  // of the present tile
+    int n0, swat, swat1;
+    const uint32_t rows_to = lds_address(&rows_lds[0][0]) + wave * 1024, w_to = lds_address(&w_lds[0][0]) + wave * 1024;
+    const uint32_t xs_to = lds_address(xs_lds) + wave * 1024, ws_to = lds_address(ws_lds) + wave * 1024;
+    // load j of steps 2 two and 2 two + 1
+    const auto load = [&](auto which, int two) {
+        constexpr int J = decltype(which)::value, V = J >> 2, C = EPI == kPlain ? J & 3 : J & 1;
+        const int past = offset_if(0, two * 2 + (chunk >> 2), steps);
+        load_to_lds(rows_src, rows_to + (two & 1) * (BM * 128) + J * 4096, (xat + J * 32 * row_bytes) | past, two * 128);
+        const int n = n0 + V * kCols<EPI, NT> + 32 * C, row = n + (EPI != kPlain && (J & 2) ? N : 0);
+        load_to_lds(w_src, w_to + (two & 1) * (BW * 128) + J * 4096, offset_if(wat, n, N) | past,
+                    row * row_bytes + two * 128);
+    };
+    // the scales of steps 8 eight .. 8 eight + 7: two threads to the 32 bytes of
+    // a row, twice
+    const int srow = tid >> 1;
+    const auto load_scales = [&](int eight) {
+        const int past = offset_if(0, eight * 8 + (tid & 1) * 4, steps), at = srow * blocks + (tid & 1) * 16;
+        load_to_lds(xs_src, xs_to, at | past, eight * 32);
+        load_to_lds(xs_src, xs_to + 4096, (at + 128 * blocks) | past, eight * 32);
+        load_to_lds(ws_src, ws_to, swat | past, eight * 32);
+        load_to_lds(ws_src, ws_to + 4096, swat1 | past, eight * 32);
+    };
+
+    // a tile's addresses and its first four steps
+    const auto begin = [&](const Tile& u) {
+        const uint32_t wrows = EPI == kPlain ? N : 2 * N;
+        rows_src = resource_words(p.x + (size_t)u.row0 * row_bytes, u.rows * row_bytes);
+        xs_src = resource_words(static_cast<const uint8_t*>(p.xs) + (size_t)u.row0 * blocks, u.rows * blocks);
+        w_src = resource_words(p.w + (size_t)u.e * wrows * row_bytes, wrows * row_bytes);
+        ws_src = resource_words(p.ws + (size_t)u.e * wrows * blocks, wrows * blocks);
+        n0 = u.n * 2 * kCols<EPI, NT>;
+        const auto at = [&](int n) {
+            const int row = weight_row<EPI, NT>(n, srow >> 4, srow & 15, N);
+            return row >= 0 ? row * blocks + (tid & 1) * 16 : kOutside;
+        };
+        swat = at(n0), swat1 = at(n0 + kCols<EPI, NT>);
+        load_scales(0);
+        each<8>([&](auto j) { load(j, 0); });
+        each<8>([&](auto j) { load(j, 1); });
+    };
+
+    f32x4 acc[MT][NT];
+    struct Operands {
+        i32x4 w[NT], x[MT];
+    } o[2];
+    struct OperandScales {
+        int w[NT], x[MT];
+    } os[2];
+    // places of chunk g of a row's first and second step
+    const int rx = (wm * 128 + m) * 8 + (g ^ (m & 7)), rw = (wn * 128 + m) * 8 + (g ^ (m & 7));
+    const auto read = [&](Operands& q, auto tile, auto step) {  // tile J of step `step` (mod 4)
+        constexpr int J = decltype(tile)::value, S = decltype(step)::value;
+        q.w[J] = w_lds[S >> 1 & 1][(S & 1 ? rw ^ 4 : rw) + J * 128];
+        q.x[J] = rows_lds[S >> 1 & 1][(S & 1 ? rx ^ 4 : rx) + J * 128];
+    };
+    // byte g of each of a row's four words of scales; past the last step 2^-127
+    // each, which leaves nothing of a product
+    const uint32_t low = 0x0C0C0400u + g * 0x0101u, high = 0x04000C0Cu + g * 0x01010000u;
+    const auto block_scales = [&](i32x4 q) {
+        return (int)(__builtin_amdgcn_perm(q.y, q.x, low) | __builtin_amdgcn_perm(q.w, q.z, high));
+    };
+    const auto scales_in = [&](int four) {
+        return (int)(uint32_t)((1ull << (8 * min(max(steps - four * 4, 0), 4))) - 1);
+    };
+    const auto read_scales = [&](i32x4& w, i32x4& x, int tile, int four) {
+        w = ws_lds[(wn * 128 + tile * 16 + m) * 2 + (four & 1)];
+        x = xs_lds[(wm * 128 + tile * 16 + m) * 2 + (four & 1)];
+    };
+
+    begin(t);
+    while (true) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // steps 0 and 1 and the scales are there; the last tile's stores need
+        // not be
+        constexpr int kStores = MT * (kCols<EPI, NT> / 32) * (EPI == kGatedMx ? 2 : 1);
+        if (v == blockIdx.x) wait_loads<16>();
+        else wait_loads<16 + kStores>();
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            i32x4 a, b;
+            read_scales(a, b, j, 0);
+            os[0].w[j] = scales_in(0) & block_scales(a), os[0].x[j] = scales_in(0) & block_scales(b);
+        }
+        each<MT>([&](auto j) { read(o[0], j, Int<0>()); });
+
+        // Step s multiplies what step s - 1 read and reads step s + 1's
+        // operands.  Two steps' rows and weights lie in a buffer, which every
+        // wavefront has read when the second of them begins: there is the
+        // barrier, and the loads of the steps three and four ahead, which have
+        // two steps' time.
+        for (int eight = 0; eight * 8 < steps; ++eight) {
+            each<8>([&](auto phase) {
+                constexpr int I = decltype(phase)::value, B = I & 1;
+                if constexpr (B == 1) {
+                    wait_loads<0>();
+                    __syncthreads();
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                // steps 3 and 7 read the next four steps' scales, a tile at a time
+                constexpr bool kScales = (I & 3) == 3;
+                const int next = eight * 2 + (I >> 2) + 1, in = scales_in(next);
+                OperandScales& then = os[1 - (I >> 2)];
+                i32x4 qw, qx;
+                each<MT>([&](auto tile) {
+                    constexpr int J = decltype(tile)::value;
+                    read(o[1 - B], tile, Int<(I + 1) & 3>());
+                    if constexpr (B == 1) load(tile, eight * 4 + (I >> 1) + 2);
+                    if constexpr (I == 5 && J == 0) load_scales(eight + 1);
+                    if constexpr (kScales) {
+                        if constexpr (J > 0) then.w[J - 1] = in & block_scales(qw), then.x[J - 1] = in & block_scales(qx);
+                        read_scales(qw, qx, J, next);
+                    }
+                    each<NT>([&](auto i) {
+                        constexpr int T = decltype(i)::value;
+                        multiply_in_place<I & 3>(acc[J][T], o[B].w[T], os[I >> 2].w[T], o[B].x[J], os[I >> 2].x[J]);
+                    });
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                if constexpr (kScales) then.w[MT - 1] = in & block_scales(qw), then.x[MT - 1] = in & block_scales(qx);
+            });
+            // the compiler does not know how long the sums take to be there
+            asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+        }
+        __syncthreads();  // LDS is free
+        const Tile done = t;
+        const int n1 = n0;
+        v += gridDim.x;
+        const bool more = table.find(ntiles, v, t);
+        if (more) begin(t);
+
+        // lane (g, m): row 16 j + m, eight columns of each 32
+        int first = wm * 128 + m;
+        asm volatile("" : "+v"(first));  // keeps 32 offsets from being held through the loop
+        const size_t width = EPI == kGatedMx ? N / 2 : N * 2;
+        const auto out = buffer_rsrc(static_cast<uint8_t*>(p.y) + (size_t)done.row0 * width,
+                                     (uint32_t)(done.rows * width));
+        const auto outs = buffer_rsrc(EPI == kGatedMx ? p.ys + (size_t)done.row0 * (N / 32) : nullptr,
+                                      EPI == kGatedMx ? (uint32_t)(done.rows * (N / 32)) : 0u);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int row = first + j * 16;
+            // the sums stay where they are until here
+#pragma unroll
+            for (int i = 0; i < NT; ++i) asm volatile("" : "+a"(acc[j][i]));
+#pragma unroll
+            for (int h = 0; h < kCols<EPI, NT> / 32; ++h) {
+                const int n = n1 + wn * kCols<EPI, NT> + 32 * h + 8 * g;
+                f32x4 a = acc[j][2 * h], b = acc[j][2 * h + 1];
+                if constexpr (EPI != kPlain) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        a[c] = gated(a[c], acc[j][2 * h + NT / 2][c]);
+                        b[c] = gated(b[c], acc[j][2 * h + 1 + NT / 2][c]);
+                    }
+                }
+                if constexpr (EPI != kGatedMx) {
+                    const i32x4 d = {(int)pack_bf16x2(a[0], a[1]), (int)pack_bf16x2(a[2], a[3]),
+                                     (int)pack_bf16x2(b[0], b[1]), (int)pack_bf16x2(b[2], b[3])};
+                    __builtin_amdgcn_raw_buffer_store_b128(d, out, n < N ? (row * N + n) * 2 : kOutside, 0, kCached);
+                } else {
+                    // the four lanes of a row hold a block of 32
+                    uint32_t x = 0u;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x = max(x, max(mag(a[c]), mag(b[c])));
+                    x = max(x, (uint32_t)__shfl_xor((int)x, 16, kWave));
+                    x = max(x, (uint32_t)__shfl_xor((int)x, 32, kWave));
+                    const uint32_t e = mx_scale(x);
+                    const uint32_t d =
+                        mx_codes4(a[0], a[1], a[2], a[3], e) | mx_codes4(b[0], b[1], b[2], b[3], e) << 16;
+                    __builtin_amdgcn_raw_buffer_store_b32((int)d, out, n < N ? (row * N + n) / 2 : kOutside, 0,
+                                                          kCached);
+                    __builtin_amdgcn_raw_buffer_store_b8(
+                        (char)e, outs, n < N && g == 0 ? row * (N / 32) + n / 32 : kOutside, 0, kCached);
+                }
+            }
+        }
+        if (!more) return;
+    }
+}
+
 // Launches one workgroup for every tile there can be (none where that many
 // cannot be launched; no receive buffer this GPU holds gets there).
 template <int BM, class Kernel>
-hipError_t launch_tiles(Kernel kernel, const Product& p, long pairs, int cols, int threads, hipStream_t stream) {
+hipError_t launch_tiles(Kernel kernel, const Product& p, long pairs, int cols, int threads, hipStream_t stream,
+                        long most = 1L << 32) {
     const int ntiles = (p.N + cols - 1) / cols;
-    const long grid = (pairs / BM + (pairs < p.rows.E ? pairs : p.rows.E)) * ntiles;
+    const long tiles = (pairs / BM + (pairs < p.rows.E ? pairs : p.rows.E)) * ntiles;
+    const long grid = tiles < most ? tiles : most;
     if (grid * threads >= 1L << 32) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(threads), 0, stream, p, ntiles);
     return hipGetLastError();
@@ -682,8 +1041,13 @@ hipError_t launch_tiles(Kernel kernel, const Product& p, long pairs, int cols, i
 template <bool FP8, int EPI>
 hipError_t launch_one(const Product& p, long pairs, hipStream_t stream) {
     if (pairs / p.rows.E < 32)
-        return launch_tiles<16>(thin_kernel<FP8, EPI, 1, 4, 2>, p, pairs, kCols<EPI>, 256, stream);
-    return launch_tiles<kTileRows>(tile_kernel<FP8, EPI>, p, pairs, kTileWaves * kCols<EPI>, kTileThreads, stream);
+        return launch_tiles<16>(thin_kernel<FP8, EPI, 1, 4, 2>, p, pairs, kCols<EPI, kThinNT>, 256, stream);
+    constexpr int cols = 2 * kCols<EPI, kTileNT>;
+    if constexpr (!FP8) {
+        if (pairs / p.rows.E >= 192 && p.K % kStep == 0)
+            return launch_tiles<kWideRows>(wide_kernel<EPI>, p, pairs, cols, kTileThreads, stream, kWideGrid);
+    }
+    return launch_tiles<128>(tile_kernel<FP8, EPI>, p, pairs, cols, kTileThreads, stream);
 }
 
 template <bool FP8>

@@ -100,6 +100,7 @@ class Case:
 
 FEW = [3, 0, 1, 16, 17, 5, 0, 33]
 MANY = [300, 0, 1, 256, 129, 64, 15, 513]
+LOTS = [300, 513, 0, 257, 400]
 
 
 @pytest.mark.parametrize("act", ["fp8", "mxfp4"])
@@ -109,6 +110,8 @@ MANY = [300, 0, 1, 256, 129, 64, 15, 513]
     ([0, 1, 0], 512, 32, 1), ([1] + [0] * 1023, 128, 32, None), ([2, 0, 1] * 33, 256, 64, None),
     (MANY, 128, 32, None), (MANY, 640, 288, None), (MANY, 1152, 352, 520), (MANY, 256, 512, 256), ([77], 384, 1024, None),
     ([40] * 12, 512, 96, None),
+    (LOTS, 128, 32, None), (LOTS, 640, 288, None), (LOTS, 1152, 352, 600), ([256] * 8, 1024, 512, None),
+    ([1000, 200], 2048, 416, None), ([222], 896, 64, None),
 ])
 def test_products(act, gate, counts, K, N, cap):
     Case(len(counts) * 1000 + K + N, counts, K, N, act, gate, cap, spare=0 if cap else 3).check("%s" % (counts[:8],))
@@ -123,7 +126,8 @@ def test_mxfp4_rows_of_any_blocks(counts, K, N, gate):
 
 @pytest.mark.parametrize("act", ["fp8", "mxfp4"])
 @pytest.mark.parametrize("counts,K,N,cap", [(FEW, 384, 96, None), (MANY, 640, 288, None), (FEW, 256, 64, 40),
-                                            ([40] * 12, 512, 96, 64)])
+                                            ([40] * 12, 512, 96, 64), (LOTS, 640, 288, None),
+                                            (LOTS, 1408, 64, 600)])
 def test_gated_to_mxfp4(act, counts, K, N, cap):
     c = Case(K + N, counts, K, N, act, True, cap, spare=0 if cap else 2)
     codes = torch.full((c.rows, N // 2), 0x5A, dtype=torch.uint8, device="cuda")
