@@ -25,14 +25,16 @@
 // 32 bits, at half the rate.
 //
 // The result has weight rows along its registers: lane (g, m) holds rows
-// 4 g .. 4 g + 3 of a 16-row weight tile for activation row m.  The 16 weight rows of a wavefront's NT tiles are chosen
-// so that a lane's NT x 4 results are consecutive columns of y: tile i, row
+// 4 g .. 4 g + 3 of a 16-row weight tile for activation row m.  The 16 weight
+// rows of a wavefront's NT tiles are chosen so that a lane's NT x 4 results are consecutive columns of y: tile i, row
 // 4 g + r is column 4 (NT g + i) + r (in the gated form, the gate tiles and
 // the up tiles each).
 //
 // How many rows an expert has is known on the device only.  Every workgroup
 // finds its tile from the counts, so nothing waits for the host; the grid is
 // an upper bound, and workgroups past the last tile end at once.
+#include <algorithm>
+
 #include "device.h"
 #include "launch.h"
 
@@ -45,7 +47,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp8 = 0, kFp4 = 4;  // matrix instruction operand formats
 constexpr int kStep = 128;         // columns of a matrix instruction
-constexpr int kThinNT = 4, kTileNT = 8;  // 16-row weight tiles per wavefront
+constexpr int kStreamNT = 4, kTileNT = 8;  // 16-row weight tiles per wavefront
 constexpr int kUnit = 127;         // E8M0 scale of 1
 
 enum Epilogue { kPlain, kGated, kGatedMx };
@@ -235,21 +237,20 @@ struct Product {
     int K, N;     // columns of x, columns of y
 };
 
-// Buffer resources of a tile's rows and of its expert's weights.
-// The rows' scales start xs_lead bytes into theirs, which is aligned to words.
-template <bool FP8, int EPI>
+// Buffer resources of a tile's MXFP4 rows and of its expert's weights.  The
+// rows' scales start xs_lead bytes into theirs, which is aligned to words.
+template <int EPI>
 struct Sources {
     __amdgpu_buffer_rsrc_t x, xs, w, ws;
     int xs_lead;
     __device__ __forceinline__ Sources(const Product& p, const Tile& t) {
-        const uint32_t xrow = FP8 ? p.K : p.K / 2, srow = FP8 ? p.K / 128 * 4 : p.K / 32;
-        const uint32_t wrows = EPI == kPlain ? p.N : 2 * p.N;
-        x = buffer_rsrc(p.x + (size_t)t.row0 * xrow, t.rows * xrow);
-        const size_t first = (size_t)t.row0 * srow;
+        const uint32_t K = p.K, wrows = EPI == kPlain ? p.N : 2 * p.N;
+        x = buffer_rsrc(p.x + (size_t)t.row0 * (K / 2), t.rows * (K / 2));
+        const size_t first = (size_t)t.row0 * (K / 32);
         xs_lead = (int)(first & 3);
-        xs = buffer_rsrc(static_cast<const uint8_t*>(p.xs) + (first - xs_lead), (t.rows * srow + xs_lead + 3) & ~3u);
-        w = buffer_rsrc(p.w + (size_t)t.e * wrows * (p.K / 2), wrows * (uint32_t)(p.K / 2));
-        ws = buffer_rsrc(p.ws + (size_t)t.e * wrows * (p.K / 32), wrows * (uint32_t)(p.K / 32));
+        xs = buffer_rsrc(static_cast<const uint8_t*>(p.xs) + (first - xs_lead), (t.rows * (K / 32) + xs_lead + 3) & ~3u);
+        w = buffer_rsrc(p.w + (size_t)t.e * wrows * (K / 2), wrows * (K / 2));
+        ws = buffer_rsrc(p.ws + (size_t)t.e * wrows * (K / 32), wrows * (K / 32));
     }
 };
 
@@ -270,175 +271,360 @@ __device__ __forceinline__ uint32_t mx_codes4(float a, float b, float c, float d
 // Largest magnitude as bits, so that a NaN among the values stays the largest.
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// -------------------------------------------------- few rows per expert
+// A buffer resource in four scalar registers, and a load from it to LDS, 16
+// bytes a lane (or one word), in the order of the lanes from byte `to` of LDS on.
+// Written out because the compiler has every later read of LDS wait for all of
+// them; wait_loads says when they are needed.  (They write no registers.)
+__device__ __forceinline__ i32x4 resource_words(const void* base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)(a >> 32)),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+template <int LANES = 64>
+__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t to, int at, int from) {
+    static_assert(LANES == 64 || LANES == 32);
+    if constexpr (LANES == 64)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :: "s"(to), "v"(at), "s"(r), "s"(from) : "memory", "m0");
+    else  // of the lower half of the lanes; every lane is on where this is called
+        asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_hi, 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds\n\t"
+                     "s_mov_b32 exec_hi, -1"
+                     :: "s"(to), "v"(at), "s"(r), "s"(from) : "memory", "m0");
+}
+template <int LANES>
+__device__ __forceinline__ void load_words_to_lds(i32x4 r, uint32_t to, int at, int from) {
+    static_assert(LANES == 64 || LANES == 32);
+    if constexpr (LANES == 64)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                     :: "s"(to), "v"(at), "s"(r), "s"(from) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_hi, 0\n\tbuffer_load_dword %1, %2, %3 offen lds\n\t"
+                     "s_mov_b32 exec_hi, -1"
+                     :: "s"(to), "v"(at), "s"(r), "s"(from) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
 
-// A workgroup takes MT x 16 rows by kCols columns; its KS wavefronts share the
-// columns of x among them, STEPS x 128 at a time in turn, and their sums are
-// added through LDS in order.  Weights and rows go straight to registers, the
-// next piece while the present one is multiplied.
-template <bool FP8, int EPI, int MT, int KS, int STEPS>
-__global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
-    constexpr int BM = 16 * MT, kNT = kThinNT;
-    __shared__ f32x4 part[KS][MT * kNT][kWave];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = lane >> 4, m = lane & 15;
-    const int K = p.K, N = p.N, steps = (K + kStep - 1) / kStep, blocks = K / 32;
+// Sources for those loads, K a multiple of 128 (a row's scales are whole words).
+template <bool FP8, int EPI>
+struct SourceWords {
+    i32x4 x, xs, w, ws;
+    __device__ __forceinline__ SourceWords() {}
+    __device__ __forceinline__ SourceWords(const Product& p, const Tile& t) {
+        const uint32_t K = p.K, row = FP8 ? K : K / 2, wrows = EPI == kPlain ? p.N : 2 * p.N;
+        x = resource_words(p.x + (size_t)t.row0 * row, t.rows * row);
+        xs = resource_words(static_cast<const uint8_t*>(p.xs) + (size_t)t.row0 * (K / 32), t.rows * (K / 32));
+        w = resource_words(p.w + (size_t)t.e * wrows * (K / 2), wrows * (K / 2));
+        ws = resource_words(p.ws + (size_t)t.e * wrows * (K / 32), wrows * (K / 32));
+    }
+};
 
-    struct Piece {
-        i32x4 w[STEPS][kNT];
-        int ws[STEPS][kNT];
-        XPiece<FP8> x[STEPS][MT];
-        int xs[STEPS][MT];
-    };
+// Waits until at most N of this wavefront's loads and stores are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
-    Tile t;
-    if (!find_tile<BM>(p.rows, ntiles, blockIdx.x, t)) return;
-    {
-        const Sources<FP8, EPI> src(p, t);
-        const int n0 = t.n * kCols<EPI, kNT>;
-        int wat[kNT], wsat[kNT], xat[MT], xsat[MT];
-#pragma unroll
-        for (int i = 0; i < kNT; ++i) {
-            const int row = weight_row<EPI, kNT>(n0, i, m, N);
-            wat[i] = row >= 0 ? row * (K / 2) + g * 16 : kOutside;
-            wsat[i] = row >= 0 ? row * blocks + g : kOutside;
-        }
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            const int row = j * 16 + m;
-            xat[j] = row * (FP8 ? K : K / 2) + g * 16;
-            xsat[j] = row < t.rows ? src.xs_lead + row * blocks + (FP8 ? 0 : g) : kOutside;
-        }
-        // past the last step (and the last block of MXFP4 rows) these read zeros
-        const auto load = [&](Piece& q, int step0) {
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int step = step0 + s, b = step * 4 + g;
-#pragma unroll
-                for (int i = 0; i < kNT; ++i) {
-                    q.w[s][i] = __builtin_amdgcn_raw_buffer_load_b128(src.w, offset_if(wat[i], b, blocks), step * 64,
-                                                                       kCached);
-                    q.ws[s][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-                        src.ws, offset_if(wsat[i], b, blocks), step * 4, kCached);
-                }
-#pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    const int xto = offset_if(xat[j], b, blocks), xsto = offset_if(xsat[j], b, blocks);
-                    q.x[s][j].v[0] =
-                        __builtin_amdgcn_raw_buffer_load_b128(src.x, xto, step * (FP8 ? 128 : 64), kCached);
-                    if constexpr (FP8) {
-                        q.x[s][j].v[1] =
-                            __builtin_amdgcn_raw_buffer_load_b128(src.x, xto + 64, step * 128, kCached);
-                        q.xs[s][j] = __builtin_amdgcn_raw_buffer_load_b32(src.xs, xsto, step * 4, kCached);
-                    } else {
-                        q.xs[s][j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.xs, xsto, step * 4, kCached);
-                    }
-                }
-            }
-        };
+// The list of rows and the tiles up to the end of each 16 experts, in LDS, for
+// kernels whose 256 threads go from tile to tile.
+template <int BM>
+struct TileTable {
+    int32_t list[1025], upto[64], part[4];
 
-        f32x4 acc[MT][kNT];
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int i = 0; i < kNT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const auto use = [&](const Piece& q) {
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-#pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    XPiece<FP8> high, low;
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            high.v[h] = upper_codes(q.x[s][j].v[h]);
-                            low.v[h] = q.x[s][j].v[h] ^ high.v[h];
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kNT; ++i) {
-                        if constexpr (FP8) {
-                            f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
-                            r = multiply<true, 0, 0>(q.w[s][i], q.ws[s][i], low, kUnit, r);
-                            r = multiply<true, 0, 0>(q.w[s][i], q.ws[s][i], high, kUnit, r);
-                            const float sc = __int_as_float(q.xs[s][j]);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) acc[j][i][c] = __builtin_fmaf(sc, r[c], acc[j][i][c]);
-                        } else {
-                            acc[j][i] = multiply<false, 0, 0>(q.w[s][i], q.ws[s][i], q.x[s][j], q.xs[s][j], acc[j][i]);
-                        }
-                    }
-                }
-            }
-        };
-        constexpr int kRun = KS * STEPS;
-        Piece a, b;
-        load(a, wave * STEPS);
-        for (int at = wave * STEPS; at < steps; at += 2 * kRun) {
-            load(b, at + kRun);
-            use(a);
-            load(a, at + 2 * kRun);
-            use(b);
-        }
+    __device__ __forceinline__ int first(const Rows& r, int e) const { return r.cap ? e * r.cap : list[e]; }
+    __device__ __forceinline__ int count(const Rows& r, int e) const {
+        return r.cap ? list[e] : max(list[e + 1] - list[e], 0);
+    }
+    __device__ __forceinline__ int tiles(const Rows& r, int e) const {
+        return e < r.E ? (count(r, e) + BM - 1) / BM : 0;
+    }
 
+    __device__ __forceinline__ void fill(const Rows& rows) {
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int i = 0; i < kNT; ++i) part[wave][j * kNT + i][lane] = acc[j][i];
+        for (int i = 0; i < 4; ++i) list[tid + i * 256] = rows.at(tid + i * 256);
+        if (tid == 0) list[1024] = rows.at(1024);
         __syncthreads();
-        const auto sum = [&](int tile, int from) {
-            f32x4 s = part[0][tile][from];
+        int mine = 0;
 #pragma unroll
-            for (int w = 1; w < KS; ++w) {
-                const f32x4 o = part[w][tile][from];
+        for (int i = 0; i < 4; ++i) mine += tiles(rows, tid * 4 + i);
+        int sum = wave_inclusive_sum(mine);
+        if (lane == 63) part[wave] = sum;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) sum += part[w];
+        if ((tid & 3) == 3) upto[tid >> 2] = sum;
+        __syncthreads();
+    }
+
+    // find_tile's order
+    __device__ __forceinline__ bool find(const Rows& rows, uint32_t ntiles, uint32_t v, Tile& t) const {
+        constexpr uint32_t kGroup = 4;
+        const int lane = threadIdx.x & 63, all = upto[lane];
+        const uint32_t n = (uint32_t)__builtin_amdgcn_readlane(all, 63) * ntiles;
+        if (v >= n) return false;
+        const uint32_t q = n >> 3, r = n & 7, x = v & 7;
+        const uint32_t at = x * q + (x < r ? x : r) + (v >> 3);
+        const int row_tile = (int)(at / ntiles);
+        const int run = __builtin_ctzll(__ballot(all > row_tile));
+        const int before = run ? __builtin_amdgcn_readlane(all, run - 1) : 0;
+        const int some = tiles(rows, run * 16 + (lane & 15));
+        const int sum = wave_inclusive_sum(some) + before;
+        const int k = __builtin_ctzll(__ballot(sum > row_tile)), e = run * 16 + k;
+        const uint32_t have = (uint32_t)__builtin_amdgcn_readlane(some, k);
+        const uint32_t start = (uint32_t)__builtin_amdgcn_readlane(sum, k) - have;
+        const uint32_t local = at - start * ntiles;
+        const uint32_t group = local / (kGroup * ntiles), in = local - group * kGroup * ntiles;
+        const uint32_t wide = min(kGroup, have - group * kGroup);
+        const int m = (int)(group * kGroup + in % wide) * BM;
+        t.e = e;
+        t.n = (int)(in / wide);
+        t.row0 = __builtin_amdgcn_readfirstlane(first(rows, e)) + m;
+        t.rows = min(BM, __builtin_amdgcn_readfirstlane(count(rows, e)) - m);
+        return true;
+    }
+};
+
+// Adds a tile's sums over KS wavefronts and stores the results: part(w, 64 (NT j
+// + i) + l) holds wavefront w's sums of row tile j, column tile i, lane l.
+template <int EPI, int MT, int NT, int KS, int THREADS, class Part>
+__device__ __forceinline__ void add_up(const Product& p, const Tile& t, int thread, Part part) {
+    const int N = p.N, n0 = t.n * kCols<EPI, NT>;
+    const auto sum = [&](int i) {
+        f32x4 s = part(0, i);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[c] += o[c];
+        for (int w = 1; w < KS; ++w) {
+            const f32x4 o = part(w, i);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[c] += o[c];
+        }
+        return s;
+    };
+    // four columns of a row to a thread, the threads of a row side by side
+    constexpr int kPer = kCols<EPI, NT> / 4;
+    static_assert(16 * kPer % kWave == 0);
+    for (int q = thread; q < 16 * MT * kPer; q += THREADS) {
+        const int row = q / kPer, c = q % kPer;  // c = 8 h + 2 g + i % 2
+        const int at = ((row >> 4) * NT + 2 * (c >> 3) + (c & 1)) * kWave + (c >> 1 & 3) * 16 + (row & 15);
+        f32x4 o = sum(at);
+        const int n = n0 + 4 * c;
+        const size_t yrow = (size_t)t.row0 + row;
+        const bool on = row < t.rows && n < N;
+        if constexpr (EPI != kPlain) {
+            const f32x4 up = sum(at + NT / 2 * kWave);
+    #pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = gated(o[i], up[i]);
+        }
+        if constexpr (EPI != kGatedMx) {
+            if (on) {
+                uint2 d;
+                d.x = pack_bf16x2(o[0], o[1]);
+                d.y = pack_bf16x2(o[2], o[3]);
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + yrow * N + n) = d;
             }
-            return s;
-        };
-        // four columns of a row to a thread, the threads of a row side by side
-        constexpr int kPer = kCols<EPI, kNT> / 4;
-        for (int q = threadIdx.x; q < BM * kPer; q += 64 * KS) {
-            const int row = q / kPer, c = q % kPer;      // c = 8 h + 2 g + i % 2
-            constexpr int kI = kNT / 2;
-            const int from = (c >> 1 & 3) * 16 + (row & 15), tile = (row >> 4) * kNT + 2 * (c >> 3) + (c & 1);
-            f32x4 o = sum(tile, from);
-            const int n = n0 + 4 * c;
-            const size_t yrow = (size_t)t.row0 + row;
-            const bool on = row < t.rows && n < N;
-            if constexpr (EPI != kPlain) {
-                const f32x4 up = sum(tile + kI, from);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = gated(o[i], up[i]);
-            }
-            if constexpr (EPI != kGatedMx) {
-                if (on) {
-                    uint2 d;
-                    d.x = pack_bf16x2(o[0], o[1]);
-                    d.y = pack_bf16x2(o[2], o[3]);
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + yrow * N + n) = d;
-                }
-            } else {
-                // eight adjacent threads hold a block of 32
-                uint32_t a = max(max(mag(o[0]), mag(o[1])), max(mag(o[2]), mag(o[3])));
-                a = max(a, dpp_u32<kDppXor1>(a));
-                a = max(a, dpp_u32<kDppXor2>(a));
-                a = max(a, dpp_u32<kDppHalfMirror>(a));
-                const uint32_t s = mx_scale(a);
-                if (on) {
-                    *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.y) + (yrow * N + n) / 2) =
-                        (uint16_t)mx_codes4(o[0], o[1], o[2], o[3], s);
-                    if (c == 0) p.ys[yrow * (N / 32) + n / 32] = (uint8_t)s;
-                }
+        } else {
+            // eight adjacent threads hold a block of 32
+            uint32_t a = max(max(mag(o[0]), mag(o[1])), max(mag(o[2]), mag(o[3])));
+            a = max(a, dpp_u32<kDppXor1>(a));
+            a = max(a, dpp_u32<kDppXor2>(a));
+            a = max(a, dpp_u32<kDppHalfMirror>(a));
+            const uint32_t s = mx_scale(a);
+            if (on) {
+                *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.y) + (yrow * N + n) / 2) =
+                    (uint16_t)mx_codes4(o[0], o[1], o[2], o[3], s);
+                if ((c & 7) == 0) p.ys[yrow * (N / 32) + n / 32] = (uint8_t)s;
             }
         }
     }
 }
 
+// -------------------------------------------------- few rows per expert
+
+// Reading the weights once is the bound.  A workgroup for each compute unit goes
+// from tile to tile: 16 MT rows by two column tiles of kCols columns, and two
+// wavefronts share a column tile's K in runs of 256 columns.  Each wavefront
+// brings its own pieces of weights, rows and scales to LDS, three deep and
+// across the ends of tiles, so that 130 KB a compute unit are in flight all the
+// time and nothing but a wavefront's own loads is waited for; eight lanes load
+// 128 consecutive bytes of a weight row.  The two sums of a tile are added
+// through LDS, in order.  K is a multiple of 128.
+//
+// Measured, 4 rows for each of 256 experts, MXFP4: K 2048, N 7168 in 330 us,
+// K 7168, N 2048 in 354 us (6.0 and 5.6 TB/s of weights; a streaming read gets
+// 7.0); with K shared by four wavefronts 356 and 334, by one 350 and 360.
+// Straight to registers, 16 bytes of 16 rows at a time, it was 560.
+constexpr int kStreamThreads = 256, kStreamShare = 2;
+
+template <bool FP8, int MT>
+struct StreamSlot {
+    i32x4 w[64 * 8];              // 16-byte chunk c of row r at c ^ (r % 8)
+    i32x4 x[16 * MT * (FP8 ? 16 : 8)];  // c ^ (r % 16), c ^ (r % 8)
+    int32_t ws[64 * 2], xs[32 * MT];   // two steps' scales of a row
+};
+
+template <bool FP8, int EPI, int MT>
+__global__ __launch_bounds__(kStreamThreads, 1) void stream_kernel(Product p, int ntiles) {
+    constexpr int NT = kStreamNT, KS = kStreamShare, kColumns = kStreamThreads / kWave / KS;
+    constexpr int kSlots = FP8 && MT > 1 ? 2 : 3, kXLoads = MT * (FP8 ? 4 : 2), kLoads = 8 + 2 + kXLoads + 1;
+    __shared__ StreamSlot<FP8, MT> ring[kStreamThreads / 64][kSlots];
+    __shared__ TileTable<16 * MT> table;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, m = lane & 15;
+    const int K = p.K, N = p.N, steps = K / kStep, blocks = K / 32, w_bytes = K / 2, x_bytes = FP8 ? K : K / 2;
+    const int pieces = ((steps + 1) / 2 + KS - 1) / KS;  // of each wavefront, some past the end
+    const int part = wave % KS, column = wave / KS, first_piece = part * pieces;
+
+    table.fill(p.rows);
+    Tile t;
+    if (!table.find(p.rows, ntiles, blockIdx.x, t)) return;
+
+    // what this lane brings: 16 bytes of weight row 8 j + lane / 8 (j = 0 .. 7),
+    // a word of scales of weight row 32 j + lane / 2, 16 bytes of a row of x and
+    // a word of its scales
+    const int wrow = 8 * (lane >> 5) + (lane >> 3 & 3), wchunk = (lane & 7) ^ (lane >> 3);
+    constexpr int kXPer = FP8 ? 16 : 8;
+    const int xrow = lane / kXPer;
+    const auto xchunk = [&](int j) { return (lane % kXPer) ^ (FP8 ? (j & 3) * 4 + xrow : xrow); };
+    const uint32_t ring_at = lds_address(&ring[wave][0]);
+    constexpr uint32_t kSize = sizeof(StreamSlot<FP8, MT>), kXAt = sizeof(i32x4) * 64 * 8;
+    constexpr uint32_t kWsAt = kXAt + sizeof(i32x4) * 16 * MT * kXPer, kXsAt = kWsAt + 512;
+
+    // the loads run ahead of the products: their tile, piece and slot
+    struct Ahead {
+        SourceWords<FP8, EPI> from;
+        int ws_at[2], n0, piece, slot;
+        uint32_t v;
+        bool have;
+    } a;
+    const auto aim = [&](const Tile& u) {
+        a.from = SourceWords<FP8, EPI>(p, u);
+        a.n0 = (u.n * kColumns + column) * kCols<EPI, NT>;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = weight_row<EPI, NT>(a.n0, 2 * j + (lane >> 5), lane >> 1 & 15, N);
+            a.ws_at[j] = row >= 0 ? row * blocks + (lane & 1) * 4 : kOutside;
+        }
+    };
+    // the tiles that the loads have reached and the products have not: two
+    // slots ahead, and each tile has a piece at least
+    static_assert(kSlots <= 3);
+    Tile next[3];
+    int ahead = 0;
+    // brings one piece; past the last one loads nothing, as many times
+    const auto bring = [&] {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
+        const int two = first_piece + a.piece, n = a.have ? steps : 0;
+        const uint32_t to = ring_at + a.slot * kSize;
+        each<8>([&](auto which) {
+            constexpr int J = decltype(which)::value, I = J >> 1, kTiles = EPI == kPlain ? NT : NT / 2, C = I % kTiles;
+            const int col = a.n0 + 32 * (C >> 1), row = col + 4 * (C & 1) + 16 * (J & 1) + (I >= kTiles ? N : 0);
+            const int at = wrow * w_bytes + wchunk * 16;
+            load_to_lds(a.from.w, to + J * 1024, offset_if(offset_if(at, two * 2 + (wchunk >> 2), n), col, N),
+                        row * w_bytes + two * 128);
+        });
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            load_words_to_lds<64>(a.from.ws, to + kWsAt + j * 256, offset_if(a.ws_at[j], two * 2 + (lane & 1), n), two * 8);
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j) {
+            const int c = xchunk(j), at = (j * (64 / kXPer) + xrow) * x_bytes + c * 16;
+            load_to_lds(a.from.x, to + kXAt + j * 1024, offset_if(at, two * 2 + c / (kXPer / 2), n), two * (16 * kXPer));
+        }
+        load_words_to_lds<32 * MT>(a.from.xs, to + kXsAt,
+                              offset_if((lane >> 1) * blocks + (lane & 1) * 4, two * 2 + (lane & 1), n), two * 8);
+        a.slot = a.slot == kSlots - 1 ? 0 : a.slot + 1;
+        if (++a.piece == pieces) {
+            a.piece = 0;
+            a.v += gridDim.x;
+            Tile u{};
+            a.have = a.have && table.find(p.rows, ntiles, a.v, u);
+            if (a.have) aim(u);
+            if (ahead == 0) next[0] = u;
+            if (ahead == 1) next[1] = u;
+            if (ahead == 2) next[2] = u;
+            ++ahead;
+        }
+    };
+
+    a.v = blockIdx.x, a.have = true, a.piece = 0, a.slot = 0;
+    aim(t);
+#pragma unroll
+    for (int i = 0; i < kSlots - 1; ++i) bring();
+    int slot = 0;
+    while (true) {
+        f32x4 acc[MT][NT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const StreamSlot<FP8, MT>* q = &ring[wave][slot];
+        for (int piece = 0; piece < pieces; ++piece) {
+            bring();  // into the slot that the last piece has left
+            wait_loads<(kSlots - 1) * kLoads>();
+            q = &ring[wave][slot];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if ((first_piece + piece) * 2 + h >= steps) break;
+                i32x4 w[NT];
+                int ws[NT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    w[i] = q->w[(i * 16 + m) * 8 + ((h * 4 + g) ^ (m & 7))];
+                    ws[i] = reinterpret_cast<const uint8_t*>(q->ws)[(i * 16 + m) * 8 + h * 4 + g];
+                }
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    const int r = j * 16 + m;
+                    if (j && t.rows <= j * 16) break;
+                    if constexpr (FP8) {
+                        XPiece<true> low, high;
+                        low.v[0] = q->x[r * 16 + ((h * 8 + g) ^ m)], low.v[1] = q->x[r * 16 + ((h * 8 + g + 4) ^ m)];
+                        const float sc = __int_as_float(q->xs[r * 2 + h]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) high.v[c] = upper_codes(low.v[c]), low.v[c] ^= high.v[c];
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+                            d = multiply<true, 0, 0>(w[i], ws[i], low, kUnit, d);
+                            d = multiply<true, 0, 0>(w[i], ws[i], high, kUnit, d);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) acc[j][i][c] = __builtin_fmaf(sc, d[c], acc[j][i][c]);
+                        }
+                    } else {
+                        XPiece<false> x;
+                        x.v[0] = q->x[r * 8 + ((h * 4 + g) ^ (m & 7))];
+                        const int xs = reinterpret_cast<const uint8_t*>(q->xs)[r * 8 + h * 4 + g];
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) acc[j][i] = multiply<false, 0, 0>(w[i], ws[i], x, xs, acc[j][i]);
+                    }
+                }
+            }
+            slot = slot == kSlots - 1 ? 0 : slot + 1;
+        }
+
+        // the sums of the four wavefronts, in the slot that was just read
+        const int last = slot == 0 ? kSlots - 1 : slot - 1;
+        f32x4* sums = reinterpret_cast<f32x4*>(ring[wave][last].w);
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sums[(j * NT + i) * 64 + lane] = acc[j][i];
+        __syncthreads();
+        t.n = t.n * kColumns + column;
+        add_up<EPI, MT, NT, KS, 64 * KS>(p, t, part * 64 + lane, [&](int w, int i) -> f32x4 {
+            return reinterpret_cast<const f32x4*>(ring[column * KS + w][last].w)[i];
+        });
+        t = next[0], next[0] = next[1], next[1] = next[2], --ahead;
+        if (t.rows == 0) break;
+        __syncthreads();
+    }
+    wait_loads<0>();  // the loads past the end write LDS too
+}
+
 // ------------------------------------------------- many rows per expert
 
-// A workgroup of 2 x 2 wavefronts takes 32 MT rows by 2 kCols columns, each
-// wavefront 16 MT rows by kCols columns.  Rows and weights of a 128-column step
+// MXFP4 rows: a workgroup of 2 x 2 wavefronts takes 32 MT rows by 2 kCols
+// columns, each wavefront 16 MT rows by kCols columns.  Rows and weights of a 128-column step
 // go through LDS (two buffers): four lanes load 64 consecutive bytes of a row,
 // where an operand straight from memory would have four lanes read 16 bytes of
 // four rows and use the cache four times over.  The scales of four steps at a
@@ -448,10 +634,10 @@ __global__ __launch_bounds__(64 * KS) void thin_kernel(Product p, int ntiles) {
 // waits.
 constexpr int kTileThreads = 256;
 
-template <bool FP8, int EPI>
+template <int EPI>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int ntiles) {
     constexpr int MT = 4, NT = kTileNT, BM = 32 * MT, BW = 32 * NT;  // rows, weight rows
-    constexpr int kChunks = FP8 ? 8 : 4;                     // 16-byte chunks of a row's step
+    constexpr int kChunks = 4;                               // 16-byte chunks of a row's step
     constexpr int kXPer = BM * kChunks / kTileThreads;       // chunks staged by a thread
     constexpr int kWPer = BW * 4 / kTileThreads;
     static_assert(BW == kTileThreads && BM <= kTileThreads);
@@ -466,21 +652,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
     // 16-byte chunk c of row r lies at a place of its own in the row, so that
     // the rows read together fall into different banks (measured: 223 bytes a
     // clock and compute unit, of 256; without it, 123)
-    const auto place8 = [](int r, int c) { return r * 8 + (c ^ (r & 7)); };
-    const auto place4 = [](int r, int c) { return r * 4 + (c ^ (r >> 1 & 3)); };
-    const auto place = [&](int r, int c) { return FP8 ? place8(r, c) : place4(r, c); };
+    const auto place = [](int r, int c) { return r * 4 + (c ^ (r >> 1 & 3)); };
 
     Tile t;
     if (!find_tile<BM>(p.rows, ntiles, blockIdx.x, t)) return;
-    const Sources<FP8, EPI> src(p, t);
+    const Sources<EPI> src(p, t);
     const int n0 = t.n * 2 * kCols<EPI, NT>;  // of the workgroup
 
     // this thread's chunks of the rows: chunk tid and those kXStride rows apart
     constexpr int kXStride = kTileThreads / kChunks;
-    const int xbytes = FP8 ? K : K / 2, xrow = tid / kChunks, xto = place(xrow, tid % kChunks);
+    const int xrow = tid / kChunks, xto = place(xrow, tid % kChunks);
     int xat[kXPer];
 #pragma unroll
-    for (int j = 0; j < kXPer; ++j) xat[j] = (xrow + j * kXStride) * xbytes + tid % kChunks * 16;
+    for (int j = 0; j < kXPer; ++j) xat[j] = (xrow + j * kXStride) * (K / 2) + tid % kChunks * 16;
     // its chunks of the weights: row 128 v + 16 i + a of LDS is wavefront column
     // v's tile i, lane row a
     const auto weight_at = [&](int r) {
@@ -492,7 +676,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
         const int row = weight_at(tid / 4 + j * (kTileThreads / 4));
         wat[j] = row >= 0 ? row * (K / 2) + (tid & 3) * 16 : kOutside;
     }
-    const int wto = place4(tid / 4, tid & 3);  // and kTileThreads / 4 rows apart
+    const int wto = place(tid / 4, tid & 3);  // and kTileThreads / 4 rows apart
     // its row's and its weight row's scales; rows of scales need not be a
     // multiple of 4 bytes
     const int sat = tid % BM * blocks + src.xs_lead, vrow = weight_at(tid);
@@ -508,7 +692,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
         constexpr int C = decltype(chunk)::value;
         if constexpr (C < kXPer)
             st[C] = __builtin_amdgcn_raw_buffer_load_b128(
-                src.x, offset_if(xat[C], step * 4 + (FP8 ? 0 : tid & 3), blocks), step * (FP8 ? 128 : 64), kCached);
+                src.x, offset_if(xat[C], step * 4 + (tid & 3), blocks), step * 64, kCached);
         else
             st[C] = __builtin_amdgcn_raw_buffer_load_b128(
                 src.w, offset_if(wat[C - kXPer], step * 4 + (tid & 3), blocks), step * 64, kCached);
@@ -534,8 +718,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
         q.more = __builtin_amdgcn_raw_buffer_load_b32(r, offset_if(at + 16, 0, row_at & 3), four * 16, kCached);
     };
     // ... zero past the row's end (those bytes are another row's), and with the
-    // steps as bytes of the blocks' words (turn) or as they are
-    const auto store_scales = [&](const Scales& q, i32x4& to, int row_at, int four, bool turn) {
+    // steps as bytes of the blocks' words
+    const auto store_scales = [&](const Scales& q, i32x4& to, int row_at, int four) {
         uint32_t d[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -543,20 +727,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
             const int n = min(max(blocks - four * 16 - s * 4, 0), 4);  // blocks of the step
             d[s] = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)row_at & 3u) & (uint32_t)((1ull << (8 * n)) - 1);
         }
-        if (turn) {
-            const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400), b = __builtin_amdgcn_perm(d[1], d[0], 0x07030602);
-            const uint32_t c = __builtin_amdgcn_perm(d[3], d[2], 0x05010400), e = __builtin_amdgcn_perm(d[3], d[2], 0x07030602);
-            to = i32x4{(int)__builtin_amdgcn_perm(c, a, 0x05040100), (int)__builtin_amdgcn_perm(c, a, 0x07060302),
-                       (int)__builtin_amdgcn_perm(e, b, 0x05040100), (int)__builtin_amdgcn_perm(e, b, 0x07060302)};
-        } else {
-            to = i32x4{(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
-        }
+        const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400), b = __builtin_amdgcn_perm(d[1], d[0], 0x07030602);
+        const uint32_t c = __builtin_amdgcn_perm(d[3], d[2], 0x05010400), e = __builtin_amdgcn_perm(d[3], d[2], 0x07030602);
+        to = i32x4{(int)__builtin_amdgcn_perm(c, a, 0x05040100), (int)__builtin_amdgcn_perm(c, a, 0x07060302),
+                   (int)__builtin_amdgcn_perm(e, b, 0x05040100), (int)__builtin_amdgcn_perm(e, b, 0x07060302)};
     };
     Scales sc;
     const auto load_row_scales = [&](int four) { load_scales(sc, src.xs, sat, four); };
     const auto load_weight_scales = [&](int four) { load_scales(sc, src.ws, vat, four); };
-    const auto store_row_scales = [&](int four) { store_scales(sc, xs_lds[four & 1][tid % BM], sat, four, !FP8); };
-    const auto store_weight_scales = [&](int four) { store_scales(sc, ws_lds[four & 1][tid], vat, four, true); };
+    const auto store_row_scales = [&](int four) { store_scales(sc, xs_lds[four & 1][tid % BM], sat, four); };
+    const auto store_weight_scales = [&](int four) { store_scales(sc, ws_lds[four & 1][tid], vat, four); };
 
     f32x4 acc[MT][NT];
 #pragma unroll
@@ -566,65 +746,43 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
 
     // this wavefront's operands: of a step, and the scales of four
     struct Operands {
-        i32x4 w[NT], x[FP8 ? 1 : MT];
+        i32x4 w[NT], x[MT];
     };
     struct OperandScales {
-        int w[NT], x[FP8 ? 1 : MT];
+        int w[NT], x[MT];
     };
     constexpr int kHalf = 16 * MT;
-    const int rx0 = place(wm * kHalf + m, g), rx1 = place(wm * kHalf + m, FP8 ? g + 4 : g);
-    const int rw = place4(wn * 128 + m, g);
+    const int rx = place(wm * kHalf + m, g), rw = place(wn * 128 + m, g);
     const auto read_scales = [&](OperandScales& o, int four) {
         const int* from = reinterpret_cast<const int*>(&ws_lds[four & 1][wn * 128 + m]) + g;
 #pragma unroll
         for (int i = 0; i < NT; ++i) o.w[i] = from[i * 64];
-        if constexpr (!FP8) {
-            const int* rows = reinterpret_cast<const int*>(&xs_lds[four & 1][wm * kHalf + m]) + g;
+        const int* rows = reinterpret_cast<const int*>(&xs_lds[four & 1][wm * kHalf + m]) + g;
 #pragma unroll
-            for (int j = 0; j < MT; ++j) o.x[j] = rows[j * 64];
-        }
+        for (int j = 0; j < MT; ++j) o.x[j] = rows[j * 64];
     };
-    const auto read_weights = [&](Operands& o, int buf) {
+    const auto read_operands = [&](Operands& o, int buf) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) o.w[i] = w_lds[buf][rw + i * 64];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) o.x[j] = rows_lds[buf][rx + j * 64];
     };
     // row tile J of step 4 four + I
-    const auto multiply_rows = [&](auto tile, auto phase, const Operands& o, const OperandScales& sc, int buf,
-                                   int four) {
+    const auto multiply_rows = [&](auto tile, auto phase, const Operands& o, const OperandScales& sc) {
         constexpr int J = decltype(tile)::value, I = decltype(phase)::value;
-        if constexpr (!FP8) {
-            each<NT>([&](auto i) {
-                constexpr int T = decltype(i)::value;
-                XPiece<false> q;
-                q.v[0] = o.x[J];
-                acc[J][T] = multiply<false, I, I>(o.w[T], sc.w[T], q, sc.x[J], acc[J][T]);
-            });
-        } else {
-            XPiece<true> low, high;
-            low.v[0] = rows_lds[buf][rx0 + J * 128], low.v[1] = rows_lds[buf][rx1 + J * 128];
-            const float xs = __int_as_float(reinterpret_cast<const int*>(&xs_lds[four & 1][wm * kHalf + J * 16 + m])[I]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) high.v[h] = upper_codes(low.v[h]), low.v[h] ^= high.v[h];
-            each<NT / 4>([&](auto quarter) {
-                constexpr int Q = decltype(quarter)::value * 4;
-                f32x4 r[4];
-                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = multiply<true, I, 0>(o.w[Q + i], sc.w[Q + i], low, kUnit, zero);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = multiply<true, I, 0>(o.w[Q + i], sc.w[Q + i], high, kUnit, r[i]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[J][Q + i][c] = __builtin_fmaf(xs, r[i][c], acc[J][Q + i][c]);
-            });
-        }
+        each<NT>([&](auto i) {
+            constexpr int T = decltype(i)::value;
+            XPiece<false> q;
+            q.v[0] = o.x[J];
+            acc[J][T] = multiply<false, I, I>(o.w[T], sc.w[T], q, sc.x[J], acc[J][T]);
+        });
     };
 
     // Step s: its operands are in LDS when every wavefront is past the barrier,
-    // and the other buffer is no longer read.  Four steps at a time, without conditions: loads past the last step read zeros,
-    // which add nothing, and each wait counts exactly what is in flight.  The
-    // scheduling barriers keep the compiler to the order of the parts.
+    // and the other buffer is no longer read.  Four steps at a time, without
+    // conditions: loads past the last step read zeros, which add nothing, and
+    // each wait counts exactly what is in flight.  The scheduling barriers keep
+    // the compiler to the order of the parts.
     load_row_scales(0);
     load_rows(0);
     load_weights(0);
@@ -633,7 +791,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
     store_rows(0);
     store_weights(0);
     load_weights(1);
-    if constexpr (!FP8) load_rows(1);
+    load_rows(1);
     store_weight_scales(0);
     load_row_scales(1);
     Operands o;
@@ -645,34 +803,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
             __syncthreads();
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (I == 0) read_scales(os, four);
-            read_weights(o, B);
-            if constexpr (FP8) {
-                // weights and rows take turns in the registers, half a step each
-                store_weights(1 - B);
-                load_rows(s + 1);
-                multiply_rows(Int<0>(), phase, o, os, B, four);
-                multiply_rows(Int<1>(), phase, o, os, B, four);
-                __builtin_amdgcn_sched_barrier(0);
-                store_rows(1 - B);
-                load_weights(s + 2);
-                multiply_rows(Int<2>(), phase, o, os, B, four);
-                multiply_rows(Int<3>(), phase, o, os, B, four);
-            } else {
-#pragma unroll
-                for (int j = 0; j < MT; ++j) o.x[j % (FP8 ? 1 : MT)] = rows_lds[B][rx0 + j * 64];
-                multiply_rows(Int<0>(), phase, o, os, B, four);
-                __builtin_amdgcn_sched_barrier(0);
-                store_rows(1 - B);
-                store_weights(1 - B);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply_rows(Int<1>(), phase, o, os, B, four);
-                __builtin_amdgcn_sched_barrier(0);
-                load_rows(s + 2);
-                load_weights(s + 2);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply_rows(Int<2>(), phase, o, os, B, four);
-                multiply_rows(Int<3>(), phase, o, os, B, four);
-            }
+            read_operands(o, B);
+            multiply_rows(Int<0>(), phase, o, os);
+            __builtin_amdgcn_sched_barrier(0);
+            store_rows(1 - B);
+            store_weights(1 - B);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply_rows(Int<1>(), phase, o, os);
+            __builtin_amdgcn_sched_barrier(0);
+            load_rows(s + 2);
+            load_weights(s + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply_rows(Int<2>(), phase, o, os);
+            multiply_rows(Int<3>(), phase, o, os);
             if constexpr (I == 0) store_row_scales(four + 1), load_weight_scales(four + 1);
             if constexpr (I == 2) store_weight_scales(four + 1), load_row_scales(four + 2);
         });
@@ -725,6 +868,186 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
     }
 }
 
+// FP8 rows: a workgroup of four wavefronts takes 128 rows by kCols columns of 16
+// weight tiles, each wavefront 32 rows by all of them, so that a row's codes are
+// split into their two halves once; with up to 64 or 32 rows, two or four
+// wavefronts share their columns.  Rows, weights and scales of a 128-column
+// step go from memory straight to LDS, one step ahead (two buffers; the scales
+// of four steps at a time).  Two workgroups share a compute unit, and one
+// multiplies while the other waits.  Row tiles past the last row are skipped.
+//
+// Both matrix instructions of a product (the two halves) and the weights'
+// way to LDS bound it: 8 experts of 4096 rows, K 7168, N 4096 take 1370 us
+// (1.40 PFLOP/s counted once, 2.8 of the 4.4 that the instruction reaches by
+// itself, at 2.0 GHz); 256 experts of 128 rows 1.6 ms, of which 1.0 without
+// the instructions and 1.25 without the loads.  Staged through registers, with
+// 64-row wavefronts, those took 1471 and 1727 us.  Loads two steps ahead, where
+// few rows leave the LDS for it, gained nothing.
+template <int EPI>
+__global__ __launch_bounds__(kTileThreads, 2) void split_kernel(Product p, int ntiles) {
+    constexpr int MT = 2, kTiles = 16, BM = 64 * MT, BW = 16 * kTiles;  // rows, weight rows
+    __shared__ i32x4 x_lds[2][BM * 8];   // 16-byte chunk c of row r at c ^ (r % 8)
+    __shared__ i32x4 w_lds[2][BW * 4];   // c ^ (r / 2 % 4)
+    __shared__ i32x4 xs_lds[2][BM], ws_lds[2][BW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, m = lane & 15;
+    const int K = p.K, N = p.N, steps = K / kStep, blocks = K / 32;
+
+    Tile t;
+    if (!find_tile<BM>(p.rows, ntiles, blockIdx.x, t)) return;
+    const int n0 = t.n * kCols<EPI, kTiles>;
+    const SourceWords<true, EPI> from(p, t);
+    // what this lane brings: of rows 32 wave + 8 j + lane / 8, of weight rows
+    // 16 (4 wave + j) + lane / 4, and the scales of rows 32 wave + lane and of
+    // weight rows 64 wave + lane
+    const int x_at = (wave * 32 + (lane >> 3)) * K + ((lane & 7) ^ (lane >> 3)) * 16;
+    const int a = lane >> 2, w_at = (8 * (a >> 2) + (a & 3)) * (K / 2) + ((lane & 3) ^ (lane >> 3 & 3)) * 16;
+    const int xs_at = (wave * 32 + lane) * blocks;
+    const int vrow = weight_row<EPI, kTiles>(n0, wave * 4 + (lane >> 4), lane & 15, N);
+    const int ws_at = vrow >= 0 ? vrow * blocks : kOutside;
+    const auto bring = [&](int buf, int step) {
+        each<4>([&](auto which) {
+            constexpr int J = decltype(which)::value;
+            load_to_lds(from.x, lds_address(&x_lds[buf][(wave * 32 + J * 8) * 8]), x_at + J * 8 * K, step * 128);
+        });
+        each<4>([&](auto which) {
+            constexpr int J = decltype(which)::value, kSame = EPI == kPlain ? kTiles : kTiles / 2;
+            const int i = wave * 4 + J, c = i & (kSame - 1);
+            const int col = n0 + 32 * (c >> 1), row = col + 4 * (c & 1) + (i >= kSame ? N : 0);
+            load_to_lds(from.w, lds_address(&w_lds[buf][i * 64]), offset_if(w_at, col, N), row * (K / 2) + step * 64);
+        });
+    };
+    const auto bring_scales = [&](int buf, int four) {
+        load_to_lds<32>(from.xs, lds_address(&xs_lds[buf][wave * 32]), xs_at, four * 16);
+        load_to_lds(from.ws, lds_address(&ws_lds[buf][wave * 64]), ws_at, four * 16);
+    };
+
+    struct Operands {
+        i32x4 w[4];
+        int ws[4];
+    };
+    // GROUPS groups of 32 rows, each group's columns shared among 4 / GROUPS
+    // wavefronts
+    const auto run = [&](auto groups) {
+        constexpr int GROUPS = decltype(groups)::value, NT = 4 * GROUPS;  // column tiles of a wavefront
+        const int row0 = wave % GROUPS * 32, share = wave / GROUPS, mine = t.rows - row0;
+        f32x4 acc[MT][NT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // its tile i in the workgroup's: gate tiles and up tiles each in a row
+        const int tile0 = EPI == kPlain ? share * NT : share * (NT / 2);
+        const auto tile_at = [&](int i) { return tile0 + i + (EPI != kPlain && i >= NT / 2 ? kTiles / 2 - NT / 2 : 0); };
+        const int xr = (row0 + m) * 8 + (g ^ (m & 7)), wr = m * 4 + (g ^ (m >> 1 & 3));
+        // the first TILES row tiles of step s
+        const auto step = [&](auto tiles, int s) {
+            constexpr int TILES = decltype(tiles)::value;
+            const int buf = s & 1, four = s >> 2 & 1;
+            const auto read = [&](Operands& o, int q) {
+                const uint8_t* scales = reinterpret_cast<const uint8_t*>(&ws_lds[four][m]) + (s & 3) * 4 + g;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o.w[i] = w_lds[buf][wr + tile_at(q * 4 + i) * 64];
+                    o.ws[i] = scales[tile_at(q * 4 + i) * 256];
+                }
+            };
+            XPiece<true> low[TILES], high[TILES];
+            float xs[TILES];
+            Operands o[2];
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) {
+                low[j].v[0] = x_lds[buf][xr + j * 128], low[j].v[1] = x_lds[buf][(xr ^ 4) + j * 128];
+                xs[j] = __int_as_float(reinterpret_cast<const int*>(&xs_lds[four][row0 + j * 16 + m])[s & 3]);
+            }
+            read(o[0], 0);
+#pragma unroll
+            for (int j = 0; j < TILES; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) high[j].v[h] = upper_codes(low[j].v[h]), low[j].v[h] ^= high[j].v[h];
+            each<GROUPS>([&](auto quarter) {
+                constexpr int Q = decltype(quarter)::value;
+                if constexpr (Q + 1 < GROUPS) read(o[1 - (Q & 1)], Q + 1);
+                const Operands& u = o[Q & 1];
+#pragma unroll
+                for (int j = 0; j < TILES; ++j) {
+                    f32x4 r[4];
+                    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = multiply<true, 0, 0>(u.w[i], u.ws[i], low[j], kUnit, zero);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = multiply<true, 0, 0>(u.w[i], u.ws[i], high[j], kUnit, r[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            acc[j][Q * 4 + i][c] = __builtin_fmaf(xs[j], r[i][c], acc[j][Q * 4 + i][c]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        bring_scales(0, 0);
+        bring(0, 0);
+        for (int s = 0; s < steps; ++s) {
+            wait_loads<0>();
+            __syncthreads();
+            if (s + 1 < steps) bring(~s & 1, s + 1);
+            if ((s & 3) == 0 && s + 4 < steps) bring_scales(~(s >> 2) & 1, (s >> 2) + 1);
+            if (mine > 16) step(Int<2>(), s);
+            else if (mine > 0) step(Int<1>(), s);
+        }
+
+        // the sums are final here, with every lane active (the matrix instructions
+        // must not move into the guarded stores below)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(acc[j][i]));
+
+        // lane (g, m): row 16 j + m, eight columns of each 32
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int row = row0 + j * 16 + m;
+            const size_t yrow = (size_t)t.row0 + row;
+#pragma unroll
+            for (int h = 0; h < kCols<EPI, NT> / 32; ++h) {
+                const int n = n0 + share * kCols<EPI, NT> + 32 * h + 8 * g;
+                const bool on = row < t.rows && n < N;
+                f32x4 a = acc[j][2 * h], b = acc[j][2 * h + 1];
+                if constexpr (EPI != kPlain) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        a[c] = gated(a[c], acc[j][2 * h + NT / 2][c]);
+                        b[c] = gated(b[c], acc[j][2 * h + 1 + NT / 2][c]);
+                    }
+                }
+                if constexpr (EPI != kGatedMx) {
+                    if (on)
+                        *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.y) + yrow * N + n) =
+                            i32x4{(int)pack_bf16x2(a[0], a[1]), (int)pack_bf16x2(a[2], a[3]),
+                                  (int)pack_bf16x2(b[0], b[1]), (int)pack_bf16x2(b[2], b[3])};
+                } else {
+                    // the four lanes of a row hold a block of 32
+                    uint32_t v = 0u;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v = max(v, max(mag(a[c]), mag(b[c])));
+                    v = max(v, (uint32_t)__shfl_xor((int)v, 16, kWave));
+                    v = max(v, (uint32_t)__shfl_xor((int)v, 32, kWave));
+                    const uint32_t e = mx_scale(v);
+                    if (on) {
+                        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + (yrow * N + n) / 2) =
+                            mx_codes4(a[0], a[1], a[2], a[3], e) | mx_codes4(b[0], b[1], b[2], b[3], e) << 16;
+                        if (g == 0) p.ys[yrow * (N / 32) + n / 32] = (uint8_t)e;
+                    }
+                }
+            }
+        }
+    };
+    if (t.rows > 64) run(Int<4>());
+    else if (t.rows > 32) run(Int<2>());
+    else run(Int<1>());
+}
+
 // ------------------------------------- many rows per expert, MXFP4 rows
 
 // A workgroup of 2 x 2 wavefronts takes 256 rows by 2 kCols columns, each
@@ -736,83 +1059,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
 // (loads complete in order).  There is one workgroup per compute unit, which
 // goes from tile to tile and starts the next tile's loads before it stores the
 // last one's results.  K is a multiple of 128.
-constexpr int kWideRows = 256, kWideGrid = 256;  // one workgroup for each of 256 compute units
-
-// Tiles before each expert, its first row and its rows, in LDS.
-struct TileTable {
-    int32_t upto[1024], first[1024], rows[1024];
-    int32_t part[4];
-
-    __device__ __forceinline__ void fill(const Rows& list) {
-        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-        int n[4], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = tid * 4 + i;
-            rows[e] = list.count(e);
-            first[e] = list.first(e);
-            n[i] = (rows[e] + kWideRows - 1) / kWideRows;
-            mine += n[i];
-        }
-        const int sum = wave_inclusive_sum(mine);
-        if (lane == 63) part[wave] = sum;
-        __syncthreads();
-        int before = sum - mine;
-        for (int w = 0; w < wave; ++w) before += part[w];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            before += n[i];
-            upto[tid * 4 + i] = before;
-        }
-        __syncthreads();
-    }
-
-    // find_tile's order
-    __device__ __forceinline__ bool find(uint32_t ntiles, uint32_t v, Tile& t) const {
-        constexpr uint32_t kGroup = 4;
-        const int lane = threadIdx.x & 63;
-        const uint32_t n = (uint32_t)__builtin_amdgcn_readfirstlane(upto[1023]) * ntiles;
-        if (v >= n) return false;
-        const uint32_t q = n >> 3, r = n & 7, x = v & 7;
-        const uint32_t at = x * q + (x < r ? x : r) + (v >> 3);
-        const int row_tile = (int)(at / ntiles);
-        const int run = __builtin_ctzll(__ballot(upto[lane * 16 + 15] > row_tile));
-        const int e = run * 16 + __builtin_ctzll(__ballot(upto[run * 16 + (lane & 15)] > row_tile));
-        const int start = e > 0 ? __builtin_amdgcn_readfirstlane(upto[e > 0 ? e - 1 : 0]) : 0;
-        const uint32_t have = (uint32_t)(__builtin_amdgcn_readfirstlane(upto[e]) - start);
-        const uint32_t local = at - (uint32_t)start * ntiles;
-        const uint32_t group = local / (kGroup * ntiles), in = local - group * kGroup * ntiles;
-        const uint32_t wide = min(kGroup, have - group * kGroup);
-        const int m = (int)(group * kGroup + in % wide) * kWideRows;
-        t.e = e;
-        t.n = (int)(in / wide);
-        t.row0 = __builtin_amdgcn_readfirstlane(first[e]) + m;
-        t.rows = min(kWideRows, __builtin_amdgcn_readfirstlane(rows[e]) - m);
-        return true;
-    }
-};
-
-// A buffer resource in four scalar registers, and a load from it to LDS, 16
-// bytes a lane, in the order of the lanes from byte `to` of LDS on.  Written
-// out because the compiler has every later read of LDS wait for all of them;
-// wait_loads says when they are needed.  (They write no registers.)
-__device__ __forceinline__ i32x4 resource_words(const void* base, uint32_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
-    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)(a >> 32)),
-                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
-}
-__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t to, int at, int from) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(to), "v"(at), "s"(r), "s"(from) : "memory", "m0");
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
-}
-
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
+constexpr int kWideRows = 256;
 
 template <int EPI>
 __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int ntiles) {
@@ -822,7 +1069,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
     __shared__ i32x4 w_lds[2][BW * 8];
     __shared__ i32x4 xs_lds[BM * 2];       // eight steps' scales of a row
     __shared__ i32x4 ws_lds[BW * 2];
-    __shared__ TileTable table;
+    __shared__ TileTable<BM> table;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, m = lane & 15, wm = wave >> 1, wn = wave & 1;
     const int K = p.K, N = p.N, steps = K / kStep, blocks = K / 32, row_bytes = K / 2;
@@ -830,7 +1077,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
     table.fill(p.rows);
     Tile t;
     uint32_t v = blockIdx.x;
-    if (!table.find(ntiles, v, t)) return;
+    if (!table.find(p.rows, ntiles, v, t)) return;
 
     // LDS is written in order of the threads, eight to the 128 bytes of a row
     // (a whole line of the cache); which 16 bytes a thread brings puts the rows
@@ -840,7 +1087,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
     const int row8 = tid >> 3, chunk = (tid & 7) ^ (row8 & 7);
     const int xat = row8 * row_bytes + chunk * 16;
     const int wat = (8 * (row8 >> 2 & 3) + 4 * (row8 >> 4) + (row8 & 3)) * row_bytes + chunk * 16;
-    i32x4 rows_src, xs_src, w_src, ws_src;  // of the present tile
+    SourceWords<false, EPI> from;  // of the present tile
     int n0, swat, swat1;
     const uint32_t rows_to = lds_address(&rows_lds[0][0]) + wave * 1024, w_to = lds_address(&w_lds[0][0]) + wave * 1024;
     const uint32_t xs_to = lds_address(xs_lds) + wave * 1024, ws_to = lds_address(ws_lds) + wave * 1024;
@@ -848,9 +1095,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
     const auto load = [&](auto which, int two) {
         constexpr int J = decltype(which)::value, V = J >> 2, C = EPI == kPlain ? J & 3 : J & 1;
         const int past = offset_if(0, two * 2 + (chunk >> 2), steps);
-        load_to_lds(rows_src, rows_to + (two & 1) * (BM * 128) + J * 4096, (xat + J * 32 * row_bytes) | past, two * 128);
+        load_to_lds(from.x, rows_to + (two & 1) * (BM * 128) + J * 4096, (xat + J * 32 * row_bytes) | past, two * 128);
         const int n = n0 + V * kCols<EPI, NT> + 32 * C, row = n + (EPI != kPlain && (J & 2) ? N : 0);
-        load_to_lds(w_src, w_to + (two & 1) * (BW * 128) + J * 4096, offset_if(wat, n, N) | past,
+        load_to_lds(from.w, w_to + (two & 1) * (BW * 128) + J * 4096, offset_if(wat, n, N) | past,
                     row * row_bytes + two * 128);
     };
     // the scales of steps 8 eight .. 8 eight + 7: two threads to the 32 bytes of
@@ -858,19 +1105,15 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
     const int srow = tid >> 1;
     const auto load_scales = [&](int eight) {
         const int past = offset_if(0, eight * 8 + (tid & 1) * 4, steps), at = srow * blocks + (tid & 1) * 16;
-        load_to_lds(xs_src, xs_to, at | past, eight * 32);
-        load_to_lds(xs_src, xs_to + 4096, (at + 128 * blocks) | past, eight * 32);
-        load_to_lds(ws_src, ws_to, swat | past, eight * 32);
-        load_to_lds(ws_src, ws_to + 4096, swat1 | past, eight * 32);
+        load_to_lds(from.xs, xs_to, at | past, eight * 32);
+        load_to_lds(from.xs, xs_to + 4096, (at + 128 * blocks) | past, eight * 32);
+        load_to_lds(from.ws, ws_to, swat | past, eight * 32);
+        load_to_lds(from.ws, ws_to + 4096, swat1 | past, eight * 32);
     };
 
     // a tile's addresses and its first four steps
     const auto begin = [&](const Tile& u) {
-        const uint32_t wrows = EPI == kPlain ? N : 2 * N;
-        rows_src = resource_words(p.x + (size_t)u.row0 * row_bytes, u.rows * row_bytes);
-        xs_src = resource_words(static_cast<const uint8_t*>(p.xs) + (size_t)u.row0 * blocks, u.rows * blocks);
-        w_src = resource_words(p.w + (size_t)u.e * wrows * row_bytes, wrows * row_bytes);
-        ws_src = resource_words(p.ws + (size_t)u.e * wrows * blocks, wrows * blocks);
+        from = SourceWords<false, EPI>(p, u);
         n0 = u.n * 2 * kCols<EPI, NT>;
         const auto at = [&](int n) {
             const int row = weight_row<EPI, NT>(n, srow >> 4, srow & 15, N);
@@ -972,7 +1215,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
         const Tile done = t;
         const int n1 = n0;
         v += gridDim.x;
-        const bool more = table.find(ntiles, v, t);
+        const bool more = table.find(p.rows, ntiles, v, t);
         if (more) begin(t);
 
         // lane (g, m): row 16 j + m, eight columns of each 32
@@ -1025,6 +1268,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
     }
 }
 
+// Workgroups of the kernels that go from tile to tile, one on a compute unit.
+constexpr long kComputeUnits = 256;
+
 // Launches one workgroup for every tile there can be (none where that many
 // cannot be launched; no receive buffer this GPU holds gets there).
 template <int BM, class Kernel>
@@ -1038,16 +1284,43 @@ hipError_t launch_tiles(Kernel kernel, const Product& p, long pairs, int cols, i
     return hipGetLastError();
 }
 
+// Which kernel, by the mean rows of an expert, which the host knows (counts are
+// on the device).  Measured in microseconds, 64 experts, K 7168, N 2048, unless
+// said otherwise:
+//   MXFP4 rows       streaming, 16 rows  32 rows  128-row tiles  256-row tiles
+//     4 (256 experts)         354           359        417
+//     24                      151           109        113
+//     30                                    113        116           119
+//     96                                    232        134           131
+//     160                                   343        191           143
+//     256                                   494        212           157
+//   FP8 rows
+//     4                       101                      106
+//     16                      111           111        109
+//     64                                    200        124
+// Where large tiles would leave compute units idle (16 experts of 64 rows),
+// streaming takes 36 of 47 and 63 of 74; with twice the rows, 61 of 51 and 119
+// of 111.
 template <bool FP8, int EPI>
 hipError_t launch_one(const Product& p, long pairs, hipStream_t stream) {
-    if (pairs / p.rows.E < 32)
-        return launch_tiles<16>(thin_kernel<FP8, EPI, 1, 4, 2>, p, pairs, kCols<EPI, kThinNT>, 256, stream);
     constexpr int cols = 2 * kCols<EPI, kTileNT>;
-    if constexpr (!FP8) {
-        if (pairs / p.rows.E >= 192 && p.K % kStep == 0)
-            return launch_tiles<kWideRows>(wide_kernel<EPI>, p, pairs, cols, kTileThreads, stream, kWideGrid);
+    const long mean = pairs / p.rows.E;
+    if (p.K % kStep == 0) {
+        // 32 rows by the columns of a large tile, one to a compute unit
+        const long units = std::max(pairs / 32, (long)p.rows.E) * ((p.N + cols - 1) / cols);
+        constexpr int narrow = kCols<EPI, kStreamNT> * kStreamThreads / kWave / kStreamShare;
+        if (mean < 12)
+            return launch_tiles<16>(stream_kernel<FP8, EPI, 1>, p, pairs, narrow, kStreamThreads, stream, kComputeUnits);
+        if (units <= kComputeUnits || (!FP8 && mean < 28))
+            return launch_tiles<32>(stream_kernel<FP8, EPI, 2>, p, pairs, narrow, kStreamThreads, stream, kComputeUnits);
     }
-    return launch_tiles<128>(tile_kernel<FP8, EPI>, p, pairs, cols, kTileThreads, stream);
+    if constexpr (FP8) {
+        return launch_tiles<128>(split_kernel<EPI>, p, pairs, cols, kTileThreads, stream);
+    } else {
+        if (mean >= 96 && p.K % kStep == 0)
+            return launch_tiles<kWideRows>(wide_kernel<EPI>, p, pairs, cols, kTileThreads, stream, kComputeUnits);
+        return launch_tiles<128>(tile_kernel<EPI>, p, pairs, cols, kTileThreads, stream);
+    }
 }
 
 template <bool FP8>

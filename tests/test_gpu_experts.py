@@ -100,6 +100,7 @@ class Case:
 
 FEW = [3, 0, 1, 16, 17, 5, 0, 33]
 MANY = [300, 0, 1, 256, 129, 64, 15, 513]
+SOME = [16, 33, 0, 1, 20, 31, 32, 17]
 LOTS = [300, 513, 0, 257, 400]
 
 
@@ -112,6 +113,11 @@ LOTS = [300, 513, 0, 257, 400]
     ([40] * 12, 512, 96, None),
     (LOTS, 128, 32, None), (LOTS, 640, 288, None), (LOTS, 1152, 352, 600), ([256] * 8, 1024, 512, None),
     ([1000, 200], 2048, 416, None), ([222], 896, 64, None),
+    (SOME, 128, 32, None), (SOME, 640, 288, None), (SOME, 1152, 352, 40), ([20] * 65, 256, 1056, None),
+    ([100, 0, 31, 64] * 16, 384, 1312, None), ([40] * 130, 384, 608, None),
+    (MANY, 128, 1824, None), (MANY, 640, 1824, None), (MANY, 384, 1824, 520),
+    (LOTS, 128, 1568, None), (LOTS, 640, 1632, None), (LOTS, 1152, 1568, 600), ([256] * 8, 1024, 1152, None),
+    ([1000, 200], 2048, 1824, None),
 ])
 def test_products(act, gate, counts, K, N, cap):
     Case(len(counts) * 1000 + K + N, counts, K, N, act, gate, cap, spare=0 if cap else 3).check("%s" % (counts[:8],))
@@ -126,6 +132,8 @@ def test_mxfp4_rows_of_any_blocks(counts, K, N, gate):
 
 @pytest.mark.parametrize("act", ["fp8", "mxfp4"])
 @pytest.mark.parametrize("counts,K,N,cap", [(FEW, 384, 96, None), (MANY, 640, 288, None), (FEW, 256, 64, 40),
+                                            (SOME, 640, 288, None), ([100, 0, 31, 64] * 16, 384, 1312, None),
+                                            (MANY, 640, 928, None), (LOTS, 384, 928, 600),
                                             ([40] * 12, 512, 96, 64), (LOTS, 640, 288, None),
                                             (LOTS, 1408, 64, 600)])
 def test_gated_to_mxfp4(act, counts, K, N, cap):
@@ -150,9 +158,9 @@ def test_gated_to_mxfp4(act, counts, K, N, cap):
 
 
 @pytest.mark.parametrize("act", ["fp8", "mxfp4"])
-@pytest.mark.parametrize("per", [4, 200])
-def test_a_nan_row_stays_alone(act, per):
-    c = Case(9, [per, per], 256, 64, act)
+@pytest.mark.parametrize("per,N", [(4, 64), (20, 64), (200, 64), (200, 5152)])
+def test_a_nan_row_stays_alone(act, per, N):
+    c = Case(9, [per, per], 256, N, act)
     if act == "fp8":
         c.x[1, 3] = 0x7F
     else:
@@ -166,22 +174,23 @@ def test_a_nan_row_stays_alone(act, per):
     assert np.array_equal(np.isnan(got), bad)
 
 
-@pytest.mark.parametrize("per", [3, 120])
-def test_offset_lists_that_lead_outside_are_clamped(per):
-    c = Case(10, [per] * 4, 256, 64, "mxfp4")
+@pytest.mark.parametrize("per,N", [(3, 64), (120, 64), (120, 4512)])
+def test_offset_lists_that_lead_outside_are_clamped(per, N):
+    c = Case(10, [per] * 4, 256, N, "mxfp4")
     good = c.list.copy()
     for at, v in ((4, 1 << 30), (0, -5)):
         c.list = good.copy()
         c.list[at] = v
         c.check("clamped list %d" % v)  # the clamped list is the right one
-    c = Case(11, [per] * 4, 256, 64, "fp8", cap=per)
+    c = Case(11, [per] * 4, 256, N, "fp8", cap=per)
     c.list[2] = 1 << 30                  # a count beyond the capacity
     c.check("clamped count")
 
 
-@pytest.mark.parametrize("per", [2, 100])
-def test_two_runs_another_stream_and_a_graph(per):
-    c = Case(12, [per] * 6, 768, 128, "fp8", True)
+@pytest.mark.parametrize("act", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("per,N", [(2, 128), (100, 128), (100, 2080)])
+def test_two_runs_another_stream_and_a_graph(per, N, act):
+    c = Case(12, [per] * 6, 768, N, act, True)
     x, xs, w, ws, li = (to_dev(v) for v in (c.x, c.xs, c.w, c.ws, c.list))
     first = ep.expert_swiglu(c.cfg, x, xs, w, ws, li)
     torch.cuda.synchronize()
