@@ -68,7 +68,8 @@ def _check(code: int, where: str) -> None:
 
 def _stream(stream, device) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return int(stream.cuda_stream)
 
 
@@ -77,6 +78,10 @@ def _ptr(t) -> int:
 
 
 def _want(t: torch.Tensor, name: str, shape, dtype, device) -> None:
+    # the usual case first: small calls are bound by these checks
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device.type != "cuda" or (device is not None and t.device != device):
@@ -433,10 +438,12 @@ def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
     _want(x, "x", x.shape, x.dtype, None)
     if codes is None:
         codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=dev)
+    else:
+        _want(codes, "codes", lead + (cols // 2,), torch.uint8, dev)
     if scales is None:
         scales = torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=dev)
-    _want(codes, "codes", lead + (cols // 2,), torch.uint8, dev)
-    _want(scales, "scales", lead + (cols // 32,), torch.uint8, dev)
+    else:
+        _want(scales, "scales", lead + (cols // 32,), torch.uint8, dev)
     kind = L.EP_TYPE_FP32 if x.dtype == torch.float32 else L.EP_TYPE_BF16
     _check(L.lib().ep_mxfp4_quantize(x.numel() // cols, cols, kind, _ptr(x), _ptr(codes), _ptr(scales),
                                      _stream(stream, dev)), "ep_mxfp4_quantize")
@@ -455,7 +462,8 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bflo
     _want(scales, "scales", lead + (cols // 32,), torch.uint8, dev)
     if out is None:
         out = torch.empty(lead + (cols,), dtype=dtype, device=dev)
-    _want(out, "out", lead + (cols,), dtype, dev)
+    else:
+        _want(out, "out", lead + (cols,), dtype, dev)
     kind = L.EP_TYPE_FP32 if dtype == torch.float32 else L.EP_TYPE_BF16
     _check(L.lib().ep_mxfp4_dequantize(codes.numel() // codes.shape[-1], cols, _ptr(codes), _ptr(scales), kind,
                                        _ptr(out), _stream(stream, dev)), "ep_mxfp4_dequantize")
@@ -481,16 +489,19 @@ def _experts(cfg: Config, capacity, x, x_scales, w, w_scales, rows_of, gate: boo
     if out_dtype == "bf16":
         if out is None:
             out = torch.empty((nrows, N), dtype=torch.bfloat16, device=dev)
-        _want(out, "out", (nrows, N), torch.bfloat16, dev)
+        else:
+            _want(out, "out", (nrows, N), torch.bfloat16, dev)
         if out_scales is not None:
             raise ValueError("out_scales must be None for bf16 output")
     elif out_dtype == "mxfp4":
         if out is None:
             out = torch.empty((nrows, N // 2), dtype=torch.uint8, device=dev)
+        else:
+            _want(out, "out", (nrows, N // 2), torch.uint8, dev)
         if out_scales is None:
             out_scales = torch.empty((nrows, N // 32), dtype=torch.uint8, device=dev)
-        _want(out, "out", (nrows, N // 2), torch.uint8, dev)
-        _want(out_scales, "out_scales", (nrows, N // 32), torch.uint8, dev)
+        else:
+            _want(out_scales, "out_scales", (nrows, N // 32), torch.uint8, dev)
     else:
         raise ValueError("out_dtype must be 'bf16' or 'mxfp4'")
     c = cfg.c()
@@ -605,7 +616,8 @@ def balance_loss_backward(cfg: Config, logits: torch.Tensor, count: torch.Tensor
     _want(grad_loss, "grad_loss", (S,), torch.float32, dev)
     if grad_logits is None:
         grad_logits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=dev)
-    _want(grad_logits, "grad_logits", (cfg.T, cfg.E), torch.float32, dev)
+    else:
+        _want(grad_logits, "grad_logits", (cfg.T, cfg.E), torch.float32, dev)
     c = cfg.c()
     _check(L.lib().ep_balance_loss_backward(ctypes.byref(c), _ptr(logits), _ptr(count), _ptr(ntok), S,
                                             _ptr(seq_offset), _ptr(mask), _ptr(grad_loss), _ptr(grad_logits),
