@@ -1,0 +1,139 @@
+"""One MoE layer on one MI355X from the package's calls, as serving and
+training would use them.
+
+  python examples/moe_layer.py [--tokens 4096] [--decode-tokens 64]
+
+Serving: the experts' weights are quantised to MXFP4 once; a step routes,
+dispatches in FP8, runs both expert products with MXFP4 rows between them, and
+combines.  Prefill takes the packed receive rows, decode the fixed-capacity
+ones.  Training: the router's balance loss by sequence joins a task loss, and
+its gradient reaches the router's weights through autograd.
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."))
+
+import combine_group_limited_amd as ep  # noqa: E402
+
+
+class BalanceLoss(torch.autograd.Function):
+    """Sum over the sequences of ep.balance_loss; the counts are constants."""
+
+    @staticmethod
+    def forward(ctx, logits, cfg, topk_idx, seq_offset):
+        r = ep.balance_loss(cfg, logits, topk_idx, seq_offset)
+        ctx.cfg, ctx.seq_offset = cfg, seq_offset
+        ctx.save_for_backward(logits, r["count"], r["ntok"])
+        return r["loss"].sum()
+
+    @staticmethod
+    def backward(ctx, grad):
+        logits, count, ntok = ctx.saved_tensors
+        per = grad.float().expand(ntok.numel()).contiguous()
+        return ep.balance_loss_backward(ctx.cfg, logits, count, ntok, per, ctx.seq_offset), None, None, None
+
+
+class MoeLayer:
+    """E experts of a gated product [H] -> [F] and a product [F] -> [H], with
+    MXFP4 weights; F a multiple of 32."""
+
+    def __init__(self, router, gate_up, down, groups=8, kept=4, k=8):
+        """router fp32 [E, H]; gate_up bf16 or fp32 [E, 2F, H], gate rows first;
+        down [E, H, F]."""
+        self.router = router
+        self.E, self.H = router.shape
+        self.shape = dict(H=self.H, E=self.E, G=groups, TG=kept, k=k, R=1)
+        self.w1 = ep.mxfp4_quantize(gate_up)
+        self.w2 = ep.mxfp4_quantize(down)
+
+    def config(self, tokens: int) -> ep.Config:
+        return ep.Config(T=tokens, **self.shape)
+
+    def prefill(self, x):
+        """x bf16 [T, H] -> bf16 [T, H], through packed receive rows."""
+        cfg = self.config(x.shape[0])
+        lay = ep.route_layout(cfg, x.float() @ self.router.t())
+        rows, scales = ep.dispatch(cfg, x, lay["slot"])
+        h, hs = ep.expert_swiglu(cfg, rows, scales, *self.w1, lay["off"], out_dtype="mxfp4")
+        y = ep.expert_product(cfg, h, hs, *self.w2, lay["off"])
+        return ep.combine(cfg, y, lay["slot"], lay["w"])
+
+    def decode(self, x):
+        """The same for few tokens: no layout pass, `T` rows for each expert."""
+        cfg, T = self.config(x.shape[0]), x.shape[0]
+        idx, w = ep.route(cfg, x.float() @ self.router.t())
+        d = ep.dispatch_ll(cfg, x, idx, T)
+        h, hs = ep.expert_swiglu_ll(cfg, T, d["recv"], d["scales"], *self.w1, d["count"], out_dtype="mxfp4")
+        y = ep.expert_product_ll(cfg, T, h, hs, *self.w2, d["count"])
+        return ep.combine_ll(cfg, T, y, d["slot"], w)
+
+    def plain(self, x, idx, w):
+        """The layer on the quantised weights with plain torch calls, without
+        the FP8 and MXFP4 roundings of the rows."""
+        g = ep.mxfp4_dequantize(*self.w1, dtype=torch.float32)
+        d = ep.mxfp4_dequantize(*self.w2, dtype=torch.float32)
+        out = torch.zeros(x.shape[0], self.H, device=x.device)
+        for e in range(self.E):
+            t, j = (idx == e).nonzero(as_tuple=True)
+            if t.numel():
+                a, b = (x[t].float() @ g[e].t()).chunk(2, dim=1)
+                out[t] += w[t, j, None] * ((torch.nn.functional.silu(a) * b) @ d[e].t())
+        return out
+
+
+def serve(tokens=4096, decode_tokens=64, H=1024, E=64, F=512, seed=0):
+    """Relative differences of prefill and decode from the plain layer."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+
+    layer = MoeLayer(rand(E, H) / H ** 0.5, rand(E, 2 * F, H) / H ** 0.5, rand(E, H, F) / F ** 0.5)
+    found = {}
+    for name, T in (("prefill", tokens), ("decode", decode_tokens)):
+        x = rand(T, H).to(torch.bfloat16)
+        out = getattr(layer, name)(x)
+        idx, w = ep.route(layer.config(T), x.float() @ layer.router.t())
+        ref = layer.plain(x, idx, w)
+        found[name] = float((out.float() - ref).norm() / ref.norm())
+    return found
+
+
+def train(tokens=2048, steps=8, H=256, E=64, seed=0, rate=2e-2):
+    """Balance loss of a router that starts biased towards few experts, step by
+    step, as its gradient alone moves the weights."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    cfg = ep.Config(T=tokens, H=H, E=E, G=8, TG=4, k=8, R=1)
+    x = torch.randn(tokens, H, generator=g, device="cuda")
+    x[:, 0] = 1.0
+    router = torch.randn(E, H, generator=g, device="cuda") / H ** 0.5
+    router[:, 0] += torch.linspace(-2, 2, E, device="cuda")
+    router.requires_grad_()
+    seq = torch.tensor([0, tokens // 3, tokens // 3, tokens], dtype=torch.int32, device="cuda")
+    opt = torch.optim.Adam([router], lr=rate)
+    losses = []
+    for _ in range(steps):
+        logits = x @ router.t()
+        idx, _ = ep.route(cfg, logits.detach())
+        loss = BalanceLoss.apply(logits, cfg, idx, seq)
+        opt.zero_grad()
+        loss.backward()
+        opt.step()
+        losses.append(loss.item())
+    return losses
+
+
+if __name__ == "__main__":
+    p = argparse.ArgumentParser()
+    p.add_argument("--tokens", type=int, default=4096)
+    p.add_argument("--decode-tokens", type=int, default=64)
+    a = p.parse_args()
+    for name, off in serve(a.tokens, a.decode_tokens).items():
+        print("%s: relative difference from the plain layer %.3f" % (name, off))
+    print("balance loss: " + " ".join("%.3f" % v for v in train(a.tokens)))
