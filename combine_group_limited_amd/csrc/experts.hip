@@ -248,7 +248,8 @@ struct Sources {
         x = buffer_rsrc(p.x + (size_t)t.row0 * (K / 2), t.rows * (K / 2));
         const size_t first = (size_t)t.row0 * (K / 32);
         xs_lead = (int)(first & 3);
-        xs = buffer_rsrc(static_cast<const uint8_t*>(p.xs) + (first - xs_lead), (t.rows * (K / 32) + xs_lead + 3) & ~3u);
+        xs = buffer_rsrc(static_cast<const uint8_t*>(p.xs) + (first - xs_lead),
+                         (t.rows * (K / 32) + xs_lead + 3) & ~3u);
         w = buffer_rsrc(p.w + (size_t)t.e * wrows * (K / 2), wrows * (K / 2));
         ws = buffer_rsrc(p.ws + (size_t)t.e * wrows * (K / 32), wrows * (K / 32));
     }
@@ -443,10 +444,10 @@ __device__ __forceinline__ void add_up(const Product& p, const Tile& t, int thre
 // Reading the weights once is the bound.  A workgroup for each compute unit goes
 // from tile to tile: 16 MT rows by two column tiles of kCols columns, and two
 // wavefronts share a column tile's K in runs of 256 columns.  Each wavefront
-// brings its own pieces of weights, rows and scales to LDS, three deep and
-// across the ends of tiles, so that 130 KB a compute unit are in flight all the
-// time and nothing but a wavefront's own loads is waited for; eight lanes load
-// 128 consecutive bytes of a weight row.  The two sums of a tile are added
+// brings its own pieces of weights, rows and scales to LDS, three deep (two with
+// 32 FP8 rows) and across the ends of tiles, so that about 90 KB a compute unit
+// are in flight all the time and nothing but a wavefront's own loads is waited
+// for; eight lanes load 128 consecutive bytes of a weight row.  The two sums of a tile are added
 // through LDS, in order.  K is a multiple of 128.
 //
 // Measured, 4 rows for each of 256 experts, MXFP4: K 2048, N 7168 in 330 us,
@@ -457,9 +458,9 @@ constexpr int kStreamThreads = 256, kStreamShare = 2;
 
 template <bool FP8, int MT>
 struct StreamSlot {
-    i32x4 w[64 * 8];              // 16-byte chunk c of row r at c ^ (r % 8)
+    i32x4 w[64 * 8];                    // 16-byte chunk c of row r at c ^ (r % 8)
     i32x4 x[16 * MT * (FP8 ? 16 : 8)];  // c ^ (r % 16), c ^ (r % 8)
-    int32_t ws[64 * 2], xs[32 * MT];   // two steps' scales of a row
+    int32_t ws[64 * 2], xs[32 * MT];    // two steps' scales of a row
 };
 
 template <bool FP8, int EPI, int MT>
@@ -505,8 +506,8 @@ __global__ __launch_bounds__(kStreamThreads, 1) void stream_kernel(Product p, in
             a.ws_at[j] = row >= 0 ? row * blocks + (lane & 1) * 4 : kOutside;
         }
     };
-    // the tiles that the loads have reached and the products have not: two
-    // slots ahead, and each tile has a piece at least
+    // the tiles that the loads have reached and the products have not: the loads
+    // are three pieces ahead at most, and each tile has a piece at least
     static_assert(kSlots <= 3);
     Tile next[3];
     int ahead = 0;
@@ -524,14 +525,16 @@ __global__ __launch_bounds__(kStreamThreads, 1) void stream_kernel(Product p, in
         });
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            load_words_to_lds<64>(a.from.ws, to + kWsAt + j * 256, offset_if(a.ws_at[j], two * 2 + (lane & 1), n), two * 8);
+            load_words_to_lds<64>(a.from.ws, to + kWsAt + j * 256, offset_if(a.ws_at[j], two * 2 + (lane & 1), n),
+                                  two * 8);
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
             const int c = xchunk(j), at = (j * (64 / kXPer) + xrow) * x_bytes + c * 16;
-            load_to_lds(a.from.x, to + kXAt + j * 1024, offset_if(at, two * 2 + c / (kXPer / 2), n), two * (16 * kXPer));
+            load_to_lds(a.from.x, to + kXAt + j * 1024, offset_if(at, two * 2 + c / (kXPer / 2), n),
+                        two * (16 * kXPer));
         }
         load_words_to_lds<32 * MT>(a.from.xs, to + kXsAt,
-                              offset_if((lane >> 1) * blocks + (lane & 1) * 4, two * 2 + (lane & 1), n), two * 8);
+                                   offset_if((lane >> 1) * blocks + (lane & 1) * 4, two * 2 + (lane & 1), n), two * 8);
         a.slot = a.slot == kSlots - 1 ? 0 : a.slot + 1;
         if (++a.piece == pieces) {
             a.piece = 0;
@@ -602,7 +605,7 @@ __global__ __launch_bounds__(kStreamThreads, 1) void stream_kernel(Product p, in
             slot = slot == kSlots - 1 ? 0 : slot + 1;
         }
 
-        // the sums of the four wavefronts, in the slot that was just read
+        // every wavefront's sums, in the slot that it has just read
         const int last = slot == 0 ? kSlots - 1 : slot - 1;
         f32x4* sums = reinterpret_cast<f32x4*>(ring[wave][last].w);
 #pragma unroll
@@ -624,14 +627,18 @@ __global__ __launch_bounds__(kStreamThreads, 1) void stream_kernel(Product p, in
 // ------------------------------------------------- many rows per expert
 
 // MXFP4 rows: a workgroup of 2 x 2 wavefronts takes 32 MT rows by 2 kCols
-// columns, each wavefront 16 MT rows by kCols columns.  Rows and weights of a 128-column step
-// go through LDS (two buffers): four lanes load 64 consecutive bytes of a row,
-// where an operand straight from memory would have four lanes read 16 bytes of
-// four rows and use the cache four times over.  The scales of four steps at a
-// time go through LDS with their 4 x 4 bytes turned, so that a lane gets the
-// four steps of its block in one word.  Every step has one barrier.
-// Two workgroups share a compute unit, and one multiplies while the other
-// waits.
+// columns, each wavefront 16 MT rows by kCols columns.  Rows and weights of a
+// 128-column step go through LDS (two buffers): four lanes load 64 consecutive
+// bytes of a row, where an operand straight from memory would have four lanes
+// read 16 bytes of four rows and use the cache four times over.  The scales of
+// four steps at a time go through LDS with their 4 x 4 bytes turned, so that a
+// lane gets the four steps of its block in one word.  Every step has one
+// barrier.  Two workgroups share a compute unit, and one multiplies while the
+// other waits.  Any K of whole blocks: what lies past the end is zero.
+//
+// Loads and staging bound it: 64 experts of 48 rows, K 7168, N 2048 take 120 us
+// (4.2 TB/s of weights), of 96 rows 134, of 256 rows 212 where the next kernel
+// takes 157.
 constexpr int kTileThreads = 256;
 
 template <int EPI>
@@ -727,8 +734,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
             const int n = min(max(blocks - four * 16 - s * 4, 0), 4);  // blocks of the step
             d[s] = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)row_at & 3u) & (uint32_t)((1ull << (8 * n)) - 1);
         }
-        const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400), b = __builtin_amdgcn_perm(d[1], d[0], 0x07030602);
-        const uint32_t c = __builtin_amdgcn_perm(d[3], d[2], 0x05010400), e = __builtin_amdgcn_perm(d[3], d[2], 0x07030602);
+        const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400);
+        const uint32_t b = __builtin_amdgcn_perm(d[1], d[0], 0x07030602);
+        const uint32_t c = __builtin_amdgcn_perm(d[3], d[2], 0x05010400);
+        const uint32_t e = __builtin_amdgcn_perm(d[3], d[2], 0x07030602);
         to = i32x4{(int)__builtin_amdgcn_perm(c, a, 0x05040100), (int)__builtin_amdgcn_perm(c, a, 0x07060302),
                    (int)__builtin_amdgcn_perm(e, b, 0x05040100), (int)__builtin_amdgcn_perm(e, b, 0x07060302)};
     };
@@ -879,8 +888,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Product p, int nt
 // Both matrix instructions of a product (the two halves) and the weights'
 // way to LDS bound it: 8 experts of 4096 rows, K 7168, N 4096 take 1370 us
 // (1.40 PFLOP/s counted once, 2.8 of the 4.4 that the instruction reaches by
-// itself, at 2.0 GHz); 256 experts of 128 rows 1.6 ms, of which 1.0 without
-// the instructions and 1.25 without the loads.  Staged through registers, with
+// itself); 256 experts of 128 rows 1.6 ms, 1.0 without the instructions and
+// 1.25 without the loads, the matrix unit busy 47% of the clocks at 1.93 GHz.  Staged through registers, with
 // 64-row wavefronts, those took 1471 and 1727 us.  Loads two steps ahead, where
 // few rows leave the LDS for it, gained nothing.
 template <int EPI>
@@ -938,7 +947,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void split_kernel(Product p, int n
             for (int i = 0; i < NT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // its tile i in the workgroup's: gate tiles and up tiles each in a row
         const int tile0 = EPI == kPlain ? share * NT : share * (NT / 2);
-        const auto tile_at = [&](int i) { return tile0 + i + (EPI != kPlain && i >= NT / 2 ? kTiles / 2 - NT / 2 : 0); };
+        const auto tile_at = [&](int i) {
+            return tile0 + i + (EPI != kPlain && i >= NT / 2 ? kTiles / 2 - NT / 2 : 0);
+        };
         const int xr = (row0 + m) * 8 + (g ^ (m & 7)), wr = m * 4 + (g ^ (m >> 1 & 3));
         // the first TILES row tiles of step s
         const auto step = [&](auto tiles, int s) {
@@ -1059,6 +1070,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void split_kernel(Product p, int n
 // (loads complete in order).  There is one workgroup per compute unit, which
 // goes from tile to tile and starts the next tile's loads before it stores the
 // last one's results.  K is a multiple of 128.
+//
+// 8 experts of 4096 rows, K 7168, N 4096 take 523 us, 3.7 PFLOP/s.  The matrix
+// unit is busy 44% of the clocks, and those are 1.96 GHz, not 2.4: instructions,
+// LDS reads and loads together reach the power limit (the instruction alone, on
+// registers, does 7.9 PFLOP/s).
 constexpr int kWideRows = 256;
 
 template <int EPI>
@@ -1197,7 +1213,8 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
                     if constexpr (B == 1) load(tile, eight * 4 + (I >> 1) + 2);
                     if constexpr (I == 5 && J == 0) load_scales(eight + 1);
                     if constexpr (kScales) {
-                        if constexpr (J > 0) then.w[J - 1] = in & block_scales(qw), then.x[J - 1] = in & block_scales(qx);
+                        if constexpr (J > 0)
+                            then.w[J - 1] = in & block_scales(qw), then.x[J - 1] = in & block_scales(qx);
                         read_scales(qw, qx, J, next);
                     }
                     each<NT>([&](auto i) {
@@ -1310,9 +1327,11 @@ hipError_t launch_one(const Product& p, long pairs, hipStream_t stream) {
         const long units = std::max(pairs / 32, (long)p.rows.E) * ((p.N + cols - 1) / cols);
         constexpr int narrow = kCols<EPI, kStreamNT> * kStreamThreads / kWave / kStreamShare;
         if (mean < 12)
-            return launch_tiles<16>(stream_kernel<FP8, EPI, 1>, p, pairs, narrow, kStreamThreads, stream, kComputeUnits);
+            return launch_tiles<16>(stream_kernel<FP8, EPI, 1>, p, pairs, narrow, kStreamThreads, stream,
+                                    kComputeUnits);
         if (units <= kComputeUnits || (!FP8 && mean < 28))
-            return launch_tiles<32>(stream_kernel<FP8, EPI, 2>, p, pairs, narrow, kStreamThreads, stream, kComputeUnits);
+            return launch_tiles<32>(stream_kernel<FP8, EPI, 2>, p, pairs, narrow, kStreamThreads, stream,
+                                    kComputeUnits);
     }
     if constexpr (FP8) {
         return launch_tiles<128>(split_kernel<EPI>, p, pairs, cols, kTileThreads, stream);

@@ -14,6 +14,10 @@
 // wavefront takes 64 blocks in four loads, in each of which 4 lanes hold a
 // block, 8 columns each.  The scales of the four loads' blocks are stored as
 // one byte per lane.
+//
+// Bound by memory: 131072 rows of 7168 bf16 columns take 384 us one way (6.2
+// TB/s read and written) and 406 us back (5.9), where a plain copy reaches 5.7
+// and a read alone 7.0; 128 rows take 2.8 us, a launch.
 #include "device.h"
 #include "launch.h"
 
