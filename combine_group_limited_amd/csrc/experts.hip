@@ -49,6 +49,7 @@ constexpr int kFp8 = 0, kFp4 = 4;  // matrix instruction operand formats
 constexpr int kStep = 128;         // columns of a matrix instruction
 constexpr int kStreamNT = 4, kTileNT = 8;  // 16-row weight tiles per wavefront
 constexpr int kUnit = 127;         // E8M0 scale of 1
+constexpr int kComputeUnits = 256;  // and workgroups of the kernels that go from tile to tile
 
 enum Epilogue { kPlain, kGated, kGatedMx };
 
@@ -181,14 +182,28 @@ struct Tile {
     int n;       // column tile
 };
 
+// Tile `local` of an expert with `have` row tiles: row tile m, column tile n.
+// Groups of four row tiles take the column tiles eight at a time, so that tiles
+// running at once share weights and rows.  A row tile's eight come one after the
+// other: workgroups go to the parts of an XCD in turn, and with an expert's row
+// tiles in turn, a nearly empty second one behind each full one, half of the
+// parts get the full ones (256 experts of 140 FP8 rows, K 7168, N 2048: 1287 us
+// that way, 1221 even with the second ones left out; this way 1160 and 784).
+__device__ __forceinline__ void place_tile(uint32_t local, uint32_t have, uint32_t ntiles, int& m, int& n) {
+    constexpr uint32_t kRows = 4, kColumns = 8;
+    const uint32_t group = local / (kRows * ntiles), rows = min(kRows, have - group * kRows);
+    uint32_t in = local - group * kRows * ntiles;
+    const uint32_t block = in / (rows * kColumns), columns = min(kColumns, ntiles - block * kColumns);
+    in -= block * rows * kColumns;
+    m = (int)(group * kRows + in / columns);
+    n = (int)(block * kColumns + in % columns);
+}
+
 // Tile number v of the launch, in XCD-contiguous order; false when there is
-// none.  Inside an expert, groups of kGroup row tiles take the column tiles in
-// turn, so that tiles running at once share weights and rows.  A lane first
-// sums the tiles of a run of experts, then the wavefront looks into the run
+// none.  A lane first sums the tiles of a run of experts, then the wavefront looks into the run
 // that holds the tile.  Every wavefront of a workgroup finds the same tile.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const Rows& rows, uint32_t ntiles, uint32_t v, Tile& t) {
-    constexpr uint32_t kGroup = 4;
     constexpr int kMost = 1024 / kWave;
     const int lane = threadIdx.x & 63, run = (rows.E + kWave - 1) / kWave;
     const auto tiles_of = [&](int e) { return (rows.count(e) + BM - 1) / BM; };
@@ -216,11 +231,9 @@ __device__ __forceinline__ bool find_tile(const Rows& rows, uint32_t ntiles, uin
     const int l = __builtin_ctzll(__ballot(upto > row_tile));
     const uint32_t have = (uint32_t)__builtin_amdgcn_readlane(mine, l);
     const uint32_t local = at - (uint32_t)__builtin_amdgcn_readlane(upto - mine, l) * ntiles;
-    const uint32_t group = local / (kGroup * ntiles), in = local - group * kGroup * ntiles;
-    const uint32_t wide = min(kGroup, have - group * kGroup);
-    const int m = (int)(group * kGroup + in % wide);
+    int m;
+    place_tile(local, have, ntiles, m, t.n);
     t.e = e0 + l;
-    t.n = (int)(in / wide);
     t.row0 = rows.first(t.e) + m * BM;
     t.rows = min(BM, rows.count(t.e) - m * BM);
     return true;
@@ -358,14 +371,19 @@ struct TileTable {
         __syncthreads();
     }
 
-    // find_tile's order
+    // find_tile's order, but an XCD's workgroups exchange their tiles from one
+    // round to the next, so that none gets an expert's last row tile each time
     __device__ __forceinline__ bool find(const Rows& rows, uint32_t ntiles, uint32_t v, Tile& t) const {
-        constexpr uint32_t kGroup = 4;
         const int lane = threadIdx.x & 63, all = upto[lane];
         const uint32_t n = (uint32_t)__builtin_amdgcn_readlane(all, 63) * ntiles;
         if (v >= n) return false;
         const uint32_t q = n >> 3, r = n & 7, x = v & 7;
-        const uint32_t at = x * q + (x < r ? x : r) + (v >> 3);
+        constexpr uint32_t kMany = kComputeUnits / 8;  // workgroups of the XCD in a full grid
+        uint32_t i = v >> 3;
+        const uint32_t round = i / kMany;
+        if (gridDim.x == kComputeUnits && (round + 1) * kMany <= q)
+            i = round * kMany + ((i + 13 * round) & (kMany - 1));
+        const uint32_t at = x * q + (x < r ? x : r) + i;
         const int row_tile = (int)(at / ntiles);
         const int run = __builtin_ctzll(__ballot(all > row_tile));
         const int before = run ? __builtin_amdgcn_readlane(all, run - 1) : 0;
@@ -375,13 +393,11 @@ struct TileTable {
         const uint32_t have = (uint32_t)__builtin_amdgcn_readlane(some, k);
         const uint32_t start = (uint32_t)__builtin_amdgcn_readlane(sum, k) - have;
         const uint32_t local = at - start * ntiles;
-        const uint32_t group = local / (kGroup * ntiles), in = local - group * kGroup * ntiles;
-        const uint32_t wide = min(kGroup, have - group * kGroup);
-        const int m = (int)(group * kGroup + in % wide) * BM;
+        int m;
+        place_tile(local, have, ntiles, m, t.n);
         t.e = e;
-        t.n = (int)(in / wide);
-        t.row0 = __builtin_amdgcn_readfirstlane(first(rows, e)) + m;
-        t.rows = min(BM, __builtin_amdgcn_readfirstlane(count(rows, e)) - m);
+        t.row0 = __builtin_amdgcn_readfirstlane(first(rows, e)) + m * BM;
+        t.rows = min(BM, __builtin_amdgcn_readfirstlane(count(rows, e)) - m * BM);
         return true;
     }
 };
@@ -1284,9 +1300,6 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
         if (!more) return;
     }
 }
-
-// Workgroups of the kernels that go from tile to tile, one on a compute unit.
-constexpr long kComputeUnits = 256;
 
 // Launches one workgroup for every tile there can be (none where that many
 // cannot be launched; no receive buffer this GPU holds gets there).
