@@ -458,19 +458,19 @@ __device__ __forceinline__ void add_up(const Product& p, const Tile& t, int thre
 // -------------------------------------------------- few rows per expert
 
 // Reading the weights once is the bound.  A workgroup for each compute unit goes
-// from tile to tile: 16 MT rows by two column tiles of kCols columns, and two
+// from tile to tile: 16 MT rows by 4 / KS column tiles of kCols columns, and KS
 // wavefronts share a column tile's K in runs of 256 columns.  Each wavefront
 // brings its own pieces of weights, rows and scales to LDS, three deep (two with
 // 32 FP8 rows) and across the ends of tiles, so that about 90 KB a compute unit
 // are in flight all the time and nothing but a wavefront's own loads is waited
-// for; eight lanes load 128 consecutive bytes of a weight row.  The two sums of a tile are added
-// through LDS, in order.  K is a multiple of 128.
+// for; eight lanes load 128 consecutive bytes of a weight row.  The KS sums of
+// a tile are added through LDS, in order.  K is a multiple of 128.
 //
 // Measured, 4 rows for each of 256 experts, MXFP4: K 2048, N 7168 in 330 us,
 // K 7168, N 2048 in 354 us (6.0 and 5.6 TB/s of weights; a streaming read gets
 // 7.0); with K shared by four wavefronts 356 and 334, by one 350 and 360.
 // Straight to registers, 16 bytes of 16 rows at a time, it was 560.
-constexpr int kStreamThreads = 256, kStreamShare = 2;
+constexpr int kStreamThreads = 256;
 
 template <bool FP8, int MT>
 struct StreamSlot {
@@ -479,9 +479,9 @@ struct StreamSlot {
     int32_t ws[64 * 2], xs[32 * MT];    // two steps' scales of a row
 };
 
-template <bool FP8, int EPI, int MT>
+template <bool FP8, int EPI, int MT, int KS>
 __global__ __launch_bounds__(kStreamThreads, 1) void stream_kernel(Product p, int ntiles) {
-    constexpr int NT = kStreamNT, KS = kStreamShare, kColumns = kStreamThreads / kWave / KS;
+    constexpr int NT = kStreamNT, kColumns = kStreamThreads / kWave / KS;
     constexpr int kSlots = FP8 && MT > 1 ? 2 : 3, kXLoads = MT * (FP8 ? 4 : 2), kLoads = 8 + 2 + kXLoads + 1;
     __shared__ StreamSlot<FP8, MT> ring[kStreamThreads / 64][kSlots];
     __shared__ TileTable<16 * MT> table;
@@ -1314,6 +1314,20 @@ hipError_t launch_tiles(Kernel kernel, const Product& p, long pairs, int cols, i
     return hipGetLastError();
 }
 
+// Four wavefronts share K where two would leave half of the compute units without
+// a tile: one row for each of 8 experts, K 7168, N 2048, FP8 rows 21.2 -> 16.6
+// us, MXFP4 17.5 -> 15.2; 64 rows, N 1024 32.3 -> 21.7 and 19.1 -> 14.1.
+template <bool FP8, int EPI, int MT>
+hipError_t launch_stream(const Product& p, long pairs, hipStream_t stream) {
+    constexpr int cols = kCols<EPI, kStreamNT>, rows = 16 * MT;
+    const long row_tiles = std::max(pairs / rows, std::min(pairs, (long)p.rows.E));
+    if (row_tiles * ((p.N + 2 * cols - 1) / (2 * cols)) <= kComputeUnits / 2)
+        return launch_tiles<rows>(stream_kernel<FP8, EPI, MT, 4>, p, pairs, cols, kStreamThreads, stream,
+                                  kComputeUnits);
+    return launch_tiles<rows>(stream_kernel<FP8, EPI, MT, 2>, p, pairs, 2 * cols, kStreamThreads, stream,
+                              kComputeUnits);
+}
+
 // Which kernel, by the mean rows of an expert, which the host knows (counts are
 // on the device).  Measured in microseconds, 64 experts, K 7168, N 2048, unless
 // said otherwise:
@@ -1338,13 +1352,8 @@ hipError_t launch_one(const Product& p, long pairs, hipStream_t stream) {
     if (p.K % kStep == 0) {
         // 32 rows by the columns of a large tile, one to a compute unit
         const long units = std::max(pairs / 32, (long)p.rows.E) * ((p.N + cols - 1) / cols);
-        constexpr int narrow = kCols<EPI, kStreamNT> * kStreamThreads / kWave / kStreamShare;
-        if (mean < 12)
-            return launch_tiles<16>(stream_kernel<FP8, EPI, 1>, p, pairs, narrow, kStreamThreads, stream,
-                                    kComputeUnits);
-        if (units <= kComputeUnits || (!FP8 && mean < 28))
-            return launch_tiles<32>(stream_kernel<FP8, EPI, 2>, p, pairs, narrow, kStreamThreads, stream,
-                                    kComputeUnits);
+        if (mean < 12) return launch_stream<FP8, EPI, 1>(p, pairs, stream);
+        if (units <= kComputeUnits || (!FP8 && mean < 28)) return launch_stream<FP8, EPI, 2>(p, pairs, stream);
     }
     if constexpr (FP8) {
         return launch_tiles<128>(split_kernel<EPI>, p, pairs, cols, kTileThreads, stream);
