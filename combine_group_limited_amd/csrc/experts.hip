@@ -26,9 +26,9 @@
 //
 // The result has weight rows along its registers: lane (g, m) holds rows
 // 4 g .. 4 g + 3 of a 16-row weight tile for activation row m.  The 16 weight
-// rows of a wavefront's NT tiles are chosen so that a lane's NT x 4 results are consecutive columns of y: tile i, row
-// 4 g + r is column 4 (NT g + i) + r (in the gated form, the gate tiles and
-// the up tiles each).
+// rows are chosen so that a lane's results of two tiles are eight consecutive
+// columns of y: tile 2 c + j, row 4 g + r is column 32 c + 8 g + 4 j + r (in the
+// gated form, the gate tiles and the up tiles each).
 //
 // How many rows an expert has is known on the device only.  Every workgroup
 // finds its tile from the counts, so nothing waits for the host; the grid is
@@ -37,6 +37,11 @@
 
 #include "device.h"
 #include "launch.h"
+
+// The loads to LDS below set m0, which is no register the compiler gives out,
+// and say so; it warns that it will not save it, and need not: it sets m0 itself
+// before any use.
+#pragma clang diagnostic ignored "-Winline-asm"
 
 namespace ep {
 
