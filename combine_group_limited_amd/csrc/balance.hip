@@ -24,9 +24,11 @@
 // it is worked on.
 //
 // Measured, 65536 tokens of 256 experts in 37 sequences: partial sums 25 us
-// (67 MB read), joining them 8, gradient 27 (67 MB read and written, 5.0 TB/s);
-// with half the workgroups 32 + 6 + 36, with twice as many 23 + 11 + 26.
-// 4096 tokens: 7 + 6 + 8; below that launches are all the time there is.
+// (67 MB read), joining them 8, gradient 26 (67 MB read and written, 5.2 TB/s).
+// With 512, 1024 and 2048 workgroups the partial sums take 32, 25 and 22 us, the
+// gradient 36, 27 and 26, and joining the sums of one sequence of that length
+// (2048 workgroups) 19 instead of 12.  4096 tokens: 7 + 6 + 8; below that
+// launches are all the time there is.
 #include "device.h"
 #include "launch.h"
 
@@ -36,7 +38,8 @@ namespace {
 
 constexpr int kThreads = 256;   // of the token kernels
 constexpr int kMinChunk = 16;   // tokens per workgroup at least
-constexpr int kChunks = 1024;   // workgroups aimed at for long batches
+constexpr int kChunks = 1024;   // workgroups aimed at for long batches,
+constexpr int kGradChunks = 2048;  // and by the gradient, which leaves no sums to join
 constexpr int kRunning = 32;    // tokens summed before they join the longer sum
 constexpr int kSlice = 32;      // experts per workgroup of the summing launch
 constexpr int kParts = 16;      // segments it sums side by side,
@@ -410,14 +413,14 @@ __global__ __launch_bounds__(kThreads) void balance_grad_kernel(const float* log
     for (int t = at + slot; t < t1; t += L::kTokens) L::store(grad + (size_t)t * E, E, sub, zero);
 }
 
-// Tokens per workgroup: 16 up to 16384 tokens, then as many as leave kChunks
-// workgroups, four to a compute unit.
-int chunk_of(int T) {
-    const int c = (T + kChunks - 1) / kChunks;
+// Tokens per workgroup: 16 up to 16 `most` tokens, then as many as leave `most`
+// workgroups.
+int chunk_of(int T, int most = kChunks) {
+    const int c = (T + most - 1) / most;
     return c <= kMinChunk ? kMinChunk : (c + kMinChunk - 1) / kMinChunk * kMinChunk;
 }
 
-int chunks_of(int T) { return (T + chunk_of(T) - 1) / chunk_of(T); }
+int chunks_of(int T, int most = kChunks) { return (T + chunk_of(T, most) - 1) / chunk_of(T, most); }
 int slices_of(int E) { return (E + kSlice - 1) / kSlice; }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -495,8 +498,9 @@ hipError_t launch_balance_grad(const Shape& s, const float* logits, int S, const
     if (s.T == 0) return hipSuccess;
     const Sequences seq{off, S, s.T};
     return with_lanes(s.E, s.E % 4 == 0 && aligned16(logits, grad), [&](auto lanes) {
-        hipLaunchKernelGGL(balance_grad_kernel<decltype(lanes)>, dim3(chunks_of(s.T)), dim3(kThreads), 0, stream,
-                           logits, mask, seq, count, ntok, grad_loss, grad, s.T, s.E, s.k, chunk_of(s.T));
+        hipLaunchKernelGGL(balance_grad_kernel<decltype(lanes)>, dim3(chunks_of(s.T, kGradChunks)), dim3(kThreads), 0,
+                           stream, logits, mask, seq, count, ntok, grad_loss, grad, s.T, s.E, s.k,
+                           chunk_of(s.T, kGradChunks));
         return hipGetLastError();
     });
 }
