@@ -1302,8 +1302,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void wide_kernel(Product p, int nt
                 }
             }
         }
-        if (!more) return;
+        if (!more) break;
     }
+    wait_loads<0>();  // the loads past the end write LDS too
 }
 
 // Launches one workgroup for every tile there can be (none where that many
