@@ -471,9 +471,8 @@ __device__ __forceinline__ void add_up(const Product& p, const Tile& t, int thre
 // for; eight lanes load 128 consecutive bytes of a weight row.  The KS sums of
 // a tile are added through LDS, in order.  K is a multiple of 128.
 //
-// Measured, 4 rows for each of 256 experts, MXFP4: K 2048, N 7168 in 330 us,
-// K 7168, N 2048 in 354 us (6.0 and 5.6 TB/s of weights; a streaming read gets
-// 7.0); with K shared by four wavefronts 356 and 334, by one 350 and 360.
+// Measured, 4 rows for each of 256 experts, MXFP4: K 2048, N 7168 in 331 us,
+// K 7168, N 2048 in 333 us (6.0 TB/s of weights; a streaming read gets 7.0).
 // Straight to registers, 16 bytes of 16 rows at a time, it was 560.
 constexpr int kStreamThreads = 256;
 
@@ -1320,25 +1319,35 @@ hipError_t launch_tiles(Kernel kernel, const Product& p, long pairs, int cols, i
     return hipGetLastError();
 }
 
-// Four wavefronts share K where two would leave half of the compute units without
-// a tile: one row for each of 8 experts, K 7168, N 2048, FP8 rows 21.2 -> 16.6
-// us, MXFP4 17.5 -> 15.2; 64 rows, N 1024 32.3 -> 21.7 and 19.1 -> 14.1.
+// How many wavefronts share a column tile's K.  The fewer, the rarer are the ends
+// of tiles, where all wait; the more, the more of a row is read at once.  4 rows
+// for each of 256 experts, N such that K N is 7.3 or 15 M, shared by 1, 2 and 4:
+//   MXFP4 rows  K 1024 178 201 241   2048 345 331 362   4096 397 392 374   7168 360 354 333 us
+//   FP8 rows    K 1024 199 244 288   2048 367 401 461   4096 416 428 454   7168 374 378 370
+// (20 MXFP4 rows for each of 64, K 2048: 56, 61, 75.)  More share it where fewer
+// would leave half of the compute units without a tile: one row for each of 8
+// experts, K 7168, N 2048, by 2 and 4: FP8 rows 21.2 and 16.6 us, MXFP4 17.5 and
+// 15.2; 64 rows, N 1024 32.3 and 21.7, 19.1 and 14.1.
 template <bool FP8, int EPI, int MT>
 hipError_t launch_stream(const Product& p, long pairs, hipStream_t stream) {
     constexpr int cols = kCols<EPI, kStreamNT>, rows = 16 * MT;
     const long row_tiles = std::max(pairs / rows, std::min(pairs, (long)p.rows.E));
-    if (row_tiles * ((p.N + 2 * cols - 1) / (2 * cols)) <= kComputeUnits / 2)
-        return launch_tiles<rows>(stream_kernel<FP8, EPI, MT, 4>, p, pairs, cols, kStreamThreads, stream,
+    int share = FP8 || p.K < 2048 * MT ? 1 : p.K < 4096 * MT ? 2 : 4;
+    const auto tiles = [&] { return row_tiles * ((p.N + 4 / share * cols - 1) / (4 / share * cols)); };
+    while (share < 4 && tiles() <= kComputeUnits / 2) share *= 2;
+    const auto launch = [&](auto ks) {
+        constexpr int KS = decltype(ks)::value;
+        return launch_tiles<rows>(stream_kernel<FP8, EPI, MT, KS>, p, pairs, 4 / KS * cols, kStreamThreads, stream,
                                   kComputeUnits);
-    return launch_tiles<rows>(stream_kernel<FP8, EPI, MT, 2>, p, pairs, 2 * cols, kStreamThreads, stream,
-                              kComputeUnits);
+    };
+    return share == 1 ? launch(Int<1>()) : share == 2 ? launch(Int<2>()) : launch(Int<4>());
 }
 
 // Which kernel, by the mean rows of an expert, which the host knows (counts are
 // on the device).  Measured in microseconds, 64 experts, K 7168, N 2048, unless
 // said otherwise:
 //   MXFP4 rows       streaming, 16 rows  32 rows  128-row tiles  256-row tiles
-//     4 (256 experts)         354           359        417
+//     4 (256 experts)         333           346        417
 //     24                      151           109        113
 //     30                                    113        116           119
 //     96                                    232        134           131

@@ -115,7 +115,7 @@ LOTS = [300, 513, 0, 257, 400]
     ([1000, 200], 2048, 416, None), ([222], 896, 64, None),
     (SOME, 128, 32, None), (SOME, 640, 288, None), (SOME, 1152, 352, 40), ([20] * 65, 256, 1056, None),
     ([100, 0, 31, 64] * 16, 384, 1312, None), ([40] * 130, 384, 608, None),
-    ([1, 0, 1, 2] * 24, 640, 1056, None), ([20, 9, 31] * 16, 896, 1120, None),
+    ([2, 0, 1] * 33, 2176, 160, None), ([20] * 65, 2176, 160, None), ([1, 0, 1, 2] * 24, 640, 1056, None), ([20, 9, 31] * 16, 896, 1120, None),
     (MANY, 128, 1824, None), (MANY, 640, 1824, None), (MANY, 384, 1824, 520),
     (LOTS, 128, 1568, None), (LOTS, 640, 1632, None), (LOTS, 1152, 1568, 600), ([256] * 8, 1024, 1152, None),
     ([1000, 200], 2048, 1824, None),
