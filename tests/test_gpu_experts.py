@@ -109,13 +109,15 @@ LOTS = [300, 513, 0, 257, 400]
 @pytest.mark.parametrize("counts,K,N,cap", [
     (FEW, 128, 32, None), (FEW, 384, 96, None), (FEW, 1280, 160, 40), (FEW, 256, 64, 8), ([1], 2944, 64, None),
     ([0, 1, 0], 512, 32, 1), ([1] + [0] * 1023, 128, 32, None), ([2, 0, 1] * 33, 256, 64, None),
-    (MANY, 128, 32, None), (MANY, 640, 288, None), (MANY, 1152, 352, 520), (MANY, 256, 512, 256), ([77], 384, 1024, None),
+    (MANY, 128, 32, None), (MANY, 640, 288, None), (MANY, 1152, 352, 520), (MANY, 256, 512, 256),
+    ([77], 384, 1024, None),
     ([40] * 12, 512, 96, None),
     (LOTS, 128, 32, None), (LOTS, 640, 288, None), (LOTS, 1152, 352, 600), ([256] * 8, 1024, 512, None),
     ([1000, 200], 2048, 416, None), ([222], 896, 64, None),
     (SOME, 128, 32, None), (SOME, 640, 288, None), (SOME, 1152, 352, 40), ([20] * 65, 256, 1056, None),
     ([100, 0, 31, 64] * 16, 384, 1312, None), ([40] * 130, 384, 608, None),
-    ([2, 0, 1] * 33, 2176, 160, None), ([20] * 65, 2176, 160, None), ([1, 0, 1, 2] * 24, 640, 1056, None), ([20, 9, 31] * 16, 896, 1120, None),
+    ([2, 0, 1] * 33, 2176, 160, None), ([20] * 65, 2176, 160, None), ([1, 0, 1, 2] * 24, 640, 1056, None),
+    ([20, 9, 31] * 16, 896, 1120, None),
     (MANY, 128, 1824, None), (MANY, 640, 1824, None), (MANY, 384, 1824, 520),
     (LOTS, 128, 1568, None), (LOTS, 640, 1632, None), (LOTS, 1152, 1568, 600), ([256] * 8, 1024, 1152, None),
     ([1000, 200], 2048, 1824, None),
